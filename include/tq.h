@@ -50,6 +50,7 @@ extern "C" {
 
 enum { TQ_Q4_K = 1, TQ_Q6_K = 2, TQ_Q8_0 = 3, TQ_Q5_K = 4, TQ_Q4_0 = 5 }; /* block formats */
 enum { TQ_F32 = 0, TQ_BF16 = 1 };                                /* dequant output types */
+enum { TQ_F16 = 2 };  /* with TQ_F32 and TQ_BF16: activation types of the tq_kv_* calls */
 enum {                                                           /* status codes */
   TQ_OK = 0,
   TQ_EINVAL = 1,       /* null pointer, unknown enum value, negative count */
@@ -365,6 +366,145 @@ int tq_chain_run(void *plan, void *stream);
  * the last call, else TQ_EDEVICE (and the error word is cleared).
  */
 int tq_chain_status(void *plan, void *stream);
+
+/* ---- a paged key/value cache held in 4 bits ---------------------------------------------------
+ * What a decode step needs between its q|k|v and its o projection: the step's page tables and
+ * slots, rotary positions, keys and values rounded to 4 bits into their slots, and attention over
+ * the cache. The cache's values are TQ_Q4_0's (blocks of 32 along the head dimension, d fp16,
+ * w = d*(n - 8)), 72 bytes for 128 values.
+ *
+ * Layout of the cache memory: pages, each holding kv_heads runs of page_tokens / 16 tiles. A tile
+ * is 16 tokens of one head: key quants, key scales, value quants, value scales. With
+ * NB = head_dim / 32 blocks b per row and W = min(NB, 4) of them a chunk (block = chunk*W + word),
+ * one byte holds a block's values i (low nibble) and i + 16 (high nibble), i < 16:
+ *   keys    [chunk][i/4][token][word][P(i%4)]         256*NB bytes
+ *   values  [chunk][token/4][i][word][P(token%4)]     256*NB bytes
+ *   scales  [token/4][block][token%4] fp16            32*NB bytes each for keys and values
+ * P = 0, 2, 1, 3. A slot is page * page_tokens + (token's place in the page). Memory of slots that
+ * hold no token may contain anything.
+ *
+ * Indices that live on the device (page numbers, slots, lengths) cannot be checked before the
+ * launch; the kernels check them: a slot outside the cache is not written (and reads as zeros), a
+ * page number outside the cache is not read (its tokens count as masked), and lengths are clamped
+ * to what the tables hold.
+ */
+typedef struct {
+  int64_t kv_heads;    /* 1..1024 */
+  int64_t head_dim;    /* 64, 96, 128 or 256 */
+  int64_t page_tokens; /* 16, 32, 64, 128, 256, 512 or 1024 */
+  int64_t pages;       /* >= 1; pages * page_tokens < 2^31 */
+  void *data;          /* device, pages * tq_kv_page_bytes() bytes, 16-byte aligned */
+} tq_kv_cache;
+
+/* Rows of heads: element (row, head, i) is data[row*row_stride + head*head_stride + i], strides in
+ * elements (>= 0; for outputs, rows and heads must not overlap). */
+typedef struct {
+  void *data; /* device, aligned to its element type */
+  int64_t heads, row_stride, head_stride;
+} tq_head_rows;
+
+/* Bytes of one page (data and pages are not looked at); 0 if the shape is invalid. */
+size_t tq_kv_page_bytes(const tq_kv_cache *cache);
+
+/*
+ * tq_kv_plan -- the page tables, slots and positions of a serving step from its requests' lengths,
+ * on the device. Request r holds kv_len[r] tokens and gets new_len[r] more; new_len -1: it has
+ * ended. With P = page_tokens, in request order:
+ *   - the pages block_table[r][0 .. ceil(kv_len/P)) of every ended request go on top of the stack
+ *     free_pages[0 .. free_count), in order;
+ *   - every further page that the other requests need for their kv_len + new_len tokens is taken
+ *     from the top of that stack (top first) and written into block_table.
+ *   cu_new    [requests + 1] first row of each request's new tokens (exclusive prefix sum)
+ *   seq_len   [requests] tokens after the step (0: ended)
+ *   slots, positions, requests_of   [rows] slot, position and request of each new token, -1 in the
+ *             rows after the last (a padded batch)
+ *   free_count_out [1] the stack's height after the step
+ *   status    [1] 0, or a sum of: 1 too few free pages; 2 more new tokens than rows; 4 a request
+ *             longer than max_blocks pages; 8 a negative length (new_len below -1) or a free_count
+ *             outside 0..pages (with the ended requests' pages). Then nothing is allocated or
+ *             released: seq_len = kv_len (0 where that is negative), every row -1, cu_new 0,
+ *             free_count_out = free_count, tables and stack unchanged.
+ * free_pages NULL (free_count and free_count_out may then be NULL too): block_table already holds
+ * the pages of the new tokens; nothing is allocated or released.
+ * No output may overlap another or an input; block_table [requests][max_blocks] and free_pages
+ * [pages] are updated in place, and a repeated call with the same kv_len, new_len and free_count
+ * gives the same result. All arrays are int32, 4-byte aligned. 1 <= requests <= 4096,
+ * 1 <= max_blocks, max_blocks * page_tokens <= 2^30, 0 <= rows < 2^28. cache->data is not looked at.
+ */
+typedef struct {
+  int64_t requests, max_blocks, rows;
+  const int32_t *kv_len, *new_len; /* [requests] */
+  int32_t *block_table;            /* [requests][max_blocks], in and out */
+  int32_t *free_pages;             /* [pages], in and out, or NULL */
+  const int32_t *free_count;       /* [1] */
+  int32_t *cu_new, *seq_len, *slots, *positions, *requests_of, *free_count_out, *status;
+} tq_kv_step;
+int tq_kv_plan(const tq_kv_cache *cache, const tq_kv_step *step, void *stream);
+
+/* Rotary positions: pair p of a head turns by positions[axis][row] * inv_freq[p] (formed in fp64),
+ * (a, b) -> (a cos - b sin, a sin + b cos). Pair p is the elements (2p, 2p+1) with interleaved
+ * set, else (p, p + pairs); elements from 2*pairs on stay. axes 1..4 (time, height, width ...):
+ * the first sections[0] pairs take their position from axis 0, the next sections[1] from axis 1,
+ * and so on; the sections add up to pairs. */
+typedef struct {
+  const float *inv_freq;    /* device [pairs] */
+  const int32_t *positions; /* device [axes][rows], axis_stride elements from axis to axis */
+  int64_t axis_stride, pairs, axes, sections[4];
+  int interleaved;
+} tq_rope;
+
+/*
+ * tq_kv_append -- for each row with a slot >= 0: turn its q heads (q to q_out) and k heads by its
+ * position (rope NULL: no turn, q must then be NULL), and round its k and v heads into the slot.
+ * A block of 32 values x (fp32; turned keys are rounded to fp32 once): m = the value of largest
+ * magnitude (the first one), d = fp16(m / -8) clamped to the finite range, n = 8 + clamp(round
+ * to nearest even(x / d), -8, 7), n = 8 where d = 0; a block with a NaN or an infinity gets
+ * d = NaN. Rows whose slot is negative or outside the cache are skipped: neither the cache nor
+ * q_out is written.
+ *   type  TQ_F32, TQ_BF16 or TQ_F16: of k, v, q and q_out. k and v have kv_heads heads; q and
+ *   q_out the same number of heads, 1..4096, or both NULL. q_out may be q (the same strides).
+ *   rows 0..2^20; the slots of one call must differ from each other where they are >= 0.
+ */
+int tq_kv_append(const tq_kv_cache *cache, int type, int64_t rows, const int32_t *slots,
+                 const tq_head_rows *k, const tq_head_rows *v, const tq_head_rows *q,
+                 const tq_head_rows *q_out, const tq_rope *rope, void *stream);
+
+/*
+ * tq_kv_read -- the keys and values at `slots` as the values they stand for, rounded once to
+ * `type`: k and v [rows][kv_heads][head_dim], 16-byte aligned (NULL: not wanted). Rows whose slot
+ * is outside the cache come out as zeros. rows 0..2^20.
+ */
+int tq_kv_read(const tq_kv_cache *cache, int type, int64_t rows, const int32_t *slots, void *k,
+               void *v, void *stream);
+
+/*
+ * tq_kv_attention -- softmax attention of the step's new tokens over the cache. Row cu_new[r] + i
+ * is token p = seq_len[r] - new + i of request r (new = cu_new[r+1] - cu_new[r]; its own key and
+ * value are in the cache already) and sees the tokens t with max(0, p - window + 1) <= t <= p
+ * (window 0: from 0), found at page block_table[r][t / page_tokens]. Head h reads kv head
+ * h / (q heads / kv_heads):
+ *   out[row][h] = sum_t softmax_t(scale * q[row][h] . k_t) v_t        (TQ type of q, rounded once)
+ *   lse[row][h] = log(sum_t exp(scale * q[row][h] . k_t))             (fp32; NULL: not wanted)
+ * A row that sees no token gets out 0 and lse -inf. Rows outside cu_new[0] .. cu_new[requests] are
+ * left as they were. fp32 sums and softmax; keys, values and queries enter the products exactly
+ * (fp32 queries to 2^-22 of the row's largest), the softmax weights times the values' scales in
+ * fp16 (TQ_BF16) or as two fp16 terms (TQ_F32, TQ_F16).
+ *   workspace: tq_kv_attention_workspace_bytes(...) bytes, 256-byte aligned, contents irrelevant;
+ *   one call at a time per workspace. rows 0..2^20, requests 1..4096, q heads a multiple of
+ *   kv_heads and at most 4096; max_blocks * page_tokens <= 2^30; scale > 0 and finite;
+ *   0 <= window < 2^31. Deterministic.
+ */
+typedef struct {
+  int64_t rows, requests, max_blocks;
+  tq_head_rows q, out;
+  float *lse; /* [rows][q heads] or NULL */
+  const int32_t *block_table, *seq_len, *cu_new;
+  float scale;
+  int64_t window;
+} tq_kv_attn;
+size_t tq_kv_attention_workspace_bytes(const tq_kv_cache *cache, int type, const tq_kv_attn *attn);
+int tq_kv_attention(const tq_kv_cache *cache, int type, const tq_kv_attn *attn, void *workspace,
+                    size_t ws_bytes, void *stream);
 
 /* Text of the last non-TQ_OK status returned on this thread ("" if none). */
 const char *tq_last_error(void);

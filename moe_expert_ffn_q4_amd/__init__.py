@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libtq.so")
 
 Q4_K, Q6_K, Q8_0, Q5_K, Q4_0 = 1, 2, 3, 4, 5
 TYPES = {"q4_k": Q4_K, "q6_k": Q6_K, "q8_0": Q8_0, "q5_k": Q5_K, "q4_0": Q4_0}
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
 PATH_AUTO, PATH_F32, PATH_BF16_MFMA = 0, 1, 2
 MOE_ROUTE, MOE_EXPERTS, MOE_COMBINE, MOE_ALL = 1, 2, 4, 7
 STATUS = {0: "TQ_OK", 1: "TQ_EINVAL", 2: "TQ_ESHAPE", 3: "TQ_EALIGN", 4: "TQ_ENOSPC",
@@ -69,6 +69,33 @@ class ChainOp(C.Structure):
                 ("y", _vp * 4), ("k", _i64), ("x", _vp)]
 
 
+class KvCacheDesc(C.Structure):
+    _fields_ = [("kv_heads", _i64), ("head_dim", _i64), ("page_tokens", _i64), ("pages", _i64),
+                ("data", _vp)]
+
+
+class HeadRows(C.Structure):
+    _fields_ = [("data", _vp), ("heads", _i64), ("row_stride", _i64), ("head_stride", _i64)]
+
+
+class KvStepDesc(C.Structure):
+    _fields_ = ([(f, _i64) for f in ("requests", "max_blocks", "rows")] +
+                [(f, _vp) for f in ("kv_len", "new_len", "block_table", "free_pages", "free_count",
+                                    "cu_new", "seq_len", "slots", "positions", "requests_of",
+                                    "free_count_out", "status")])
+
+
+class RopeDesc(C.Structure):
+    _fields_ = [("inv_freq", _vp), ("positions", _vp), ("axis_stride", _i64), ("pairs", _i64),
+                ("axes", _i64), ("sections", _i64 * 4), ("interleaved", _int)]
+
+
+class KvAttnDesc(C.Structure):
+    _fields_ = [("rows", _i64), ("requests", _i64), ("max_blocks", _i64), ("q", HeadRows),
+                ("out", HeadRows), ("lse", _vp), ("block_table", _vp), ("seq_len", _vp),
+                ("cu_new", _vp), ("scale", C.c_float), ("window", _i64)]
+
+
 class MoeRouting(C.Structure):
     _fields_ = [("topk_ids", _vp), ("topk_w", _vp), ("logits", _vp), ("counts", _vp),
                 ("offsets", _vp), ("pairs", _vp)]
@@ -110,6 +137,18 @@ def _declare(L: C.CDLL) -> None:
     L.tq_chain_run.restype = _int
     L.tq_chain_status.argtypes = [_vp, _vp]
     L.tq_chain_status.restype = _int
+    L.tq_kv_page_bytes.argtypes = [_vp]
+    L.tq_kv_page_bytes.restype = C.c_size_t
+    L.tq_kv_plan.argtypes = [_vp, _vp, _vp]
+    L.tq_kv_plan.restype = _int
+    L.tq_kv_append.argtypes = [_vp, _int, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+    L.tq_kv_append.restype = _int
+    L.tq_kv_read.argtypes = [_vp, _int, _i64, _vp, _vp, _vp, _vp]
+    L.tq_kv_read.restype = _int
+    L.tq_kv_attention_workspace_bytes.argtypes = [_vp, _int, _vp]
+    L.tq_kv_attention_workspace_bytes.restype = C.c_size_t
+    L.tq_kv_attention.argtypes = [_vp, _int, _vp, _vp, C.c_size_t, _vp]
+    L.tq_kv_attention.restype = _int
     if hasattr(L, "tq_moe_ffn"):
         L.tq_moe_workspace_bytes.argtypes = [C.POINTER(MoeDesc), _i64]
         L.tq_moe_workspace_bytes.restype = C.c_size_t
@@ -411,6 +450,249 @@ class ExpertCache:
             torch.cuda.synchronize()
             _check(lib().tq_expert_cache_destroy(self.state_ptr))
             self.open = False
+
+
+# ---- a paged key/value cache held in 4 bits (tq_kv_*) --------------------------------------------
+
+ACT_TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _kv_tensor(t, name: str, dtype, shape, device, strided: bool = False):
+    """Checks a tensor argument of a tq_kv_* call: dtype, shape (None: any), device, density."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if len(shape) != t.dim() or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have the shape {list(shape)}, not {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if strided:
+        if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"the last dimension of {name} must be dense")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+class _On:
+    """The cache's device and the call's stream as the current ones, where they are not already:
+    outputs and workspaces that a call makes then belong to the stream that uses them. `.handle`
+    is the stream."""
+
+    __slots__ = ("ctx", "handle")
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"the cache is on {device}, not on a GPU")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the cache on {device}")
+        self.ctx = None
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != device.index:
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        self.handle = torch.cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+
+class KvCache:
+    """Pages of keys and values held as 4-bit blocks (tq_kv_cache). Makes its memory (`pages` on
+    `device`; uint8 [pages, page bytes], contents irrelevant until written) or takes `data`.
+    head_dim 64, 96, 128 or 256; page_tokens 16, 32, ... 1024."""
+
+    def __init__(self, kv_heads: int, head_dim: int, page_tokens: int, pages: int | None = None,
+                 data: torch.Tensor | None = None, device=None):
+        d = KvCacheDesc(kv_heads, head_dim, page_tokens, 1, None)
+        self.page_bytes = int(lib().tq_kv_page_bytes(C.byref(d)))
+        if not self.page_bytes:
+            raise ValueError(f"a cache of {kv_heads} heads of {head_dim} in pages of {page_tokens} "
+                             "tokens is not supported")
+        if (pages is None) == (data is None):
+            raise ValueError("give either pages or data")
+        if data is None:
+            data = torch.empty((pages, self.page_bytes), dtype=torch.uint8,
+                               device=device if device is not None else "cuda")
+        else:
+            _kv_tensor(data, "data", torch.uint8, (None, self.page_bytes), data.device)
+        self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
+        self.data, self.pages, self.device = data, data.shape[0], data.device
+        d.pages, d.data = self.pages, data.data_ptr()
+        self.desc = d
+        self.ref = C.byref(d)
+
+
+class Rope:
+    """Rotary positions: inv_freq fp32 [pairs]; sections: how many pairs take their position from
+    each axis (default: all from one); interleaved: pairs (2p, 2p + 1), else (p, p + pairs)."""
+
+    def __init__(self, inv_freq: torch.Tensor, sections=None, interleaved: bool = False):
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a dense fp32 vector")
+        self.inv_freq, self.pairs = inv_freq, inv_freq.shape[0]
+        self.sections = [self.pairs] if sections is None else [int(n) for n in sections]
+        if not 1 <= len(self.sections) <= 4 or min(self.sections) < 0 or sum(self.sections) != self.pairs:
+            raise ValueError(f"sections {self.sections} must be 1 to 4 counts that add up to {self.pairs}")
+        self.interleaved = bool(interleaved)
+        self.desc = RopeDesc(inv_freq.data_ptr(), None, 0, self.pairs, len(self.sections),
+                             (_i64 * 4)(*self.sections), int(interleaved))
+
+
+def _head_rows(t: torch.Tensor) -> HeadRows:
+    rs, hs, _ = t.stride()
+    return HeadRows(t.data_ptr(), t.shape[1], rs, hs)
+
+
+def kv_plan(cache: KvCache, kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor,
+            rows: int, free_pages: torch.Tensor | None = None,
+            free_count: torch.Tensor | None = None, stream=None) -> dict:
+    """Tables, slots and positions of a step from its requests' lengths (tq_kv_plan): new_len[r]
+    more tokens for request r, or -1 when it has ended. block_table [requests, max_blocks] and
+    free_pages [pages] are updated in place (free_pages None: the table already holds the new
+    tokens' pages). Returns a dict with block_table, cu_new, seq_len, slots, positions, requests
+    (int32; -1 in the rows after the last token), free_pages, free_count (the new one) and status
+    [1], on the device: 0, or the sum of reasons why nothing was done (1 pages, 2 rows, 4 table
+    columns, 8 lengths)."""
+    R, dev, i32 = kv_len.shape[0], cache.device, torch.int32
+    _kv_tensor(kv_len, "kv_len", i32, (None,), dev)
+    _kv_tensor(new_len, "new_len", i32, (R,), dev)
+    _kv_tensor(block_table, "block_table", i32, (R, None), dev)
+    if (free_pages is None) != (free_count is None):
+        raise ValueError("free_pages and free_count go together")
+    if free_pages is not None:
+        _kv_tensor(free_pages, "free_pages", i32, (cache.pages,), dev)
+        _kv_tensor(free_count, "free_count", i32, (1,), dev)
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    with _On(dev, stream) as on:
+        out = torch.empty(2 * R + 3 + 3 * rows, dtype=i32, device=dev)
+        cu, seq, count, status, slots, pos, req = out.split([R + 1, R, 1, 1, rows, rows, rows])
+        base = out.data_ptr()
+        at = base + 4 * (2 * R + 3)
+        d = KvStepDesc(R, block_table.shape[1], rows, kv_len.data_ptr(), new_len.data_ptr(),
+                       block_table.data_ptr(), _ptr(free_pages), _ptr(free_count), base,
+                       base + 4 * (R + 1), at if rows else None, at + 4 * rows if rows else None,
+                       at + 8 * rows if rows else None,
+                       base + 4 * (2 * R + 1) if free_pages is not None else None,
+                       base + 4 * (2 * R + 2))
+        _check(lib().tq_kv_plan(cache.ref, C.byref(d), on.handle))
+    res = {"block_table": block_table, "cu_new": cu, "seq_len": seq, "slots": slots,
+           "positions": pos, "requests": req, "status": status}
+    if free_pages is not None:
+        res["free_pages"], res["free_count"] = free_pages, count
+    return res
+
+
+def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+              q: torch.Tensor | None = None, rope: Rope | None = None,
+              positions: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+              stream=None):
+    """Rounds the rows k, v [rows, kv_heads, head_dim] (fp32, bf16 or fp16; rows and heads at any
+    stride) into their slots, keys and the queries q [rows, heads, head_dim] turned by `rope` at
+    `positions` (int32 [rows] or [axes, rows]) (tq_kv_append). Returns the turned queries (q_out,
+    which may be q; rows with slot -1 are left as they were), or None without q."""
+    dev, D = cache.device, cache.head_dim
+    if not isinstance(k, torch.Tensor) or k.dtype not in ACT_TYPES:
+        raise ValueError("k must be a tensor of fp32, bf16 or fp16")
+    rows = k.shape[0]
+    _kv_tensor(k, "k", k.dtype, (rows, cache.kv_heads, D), dev, strided=True)
+    _kv_tensor(v, "v", k.dtype, (rows, cache.kv_heads, D), dev, strided=True)
+    _kv_tensor(slots, "slots", torch.int32, (rows,), dev)
+    if (rope is None) != (positions is None):
+        raise ValueError("rope and positions go together")
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    if q is not None and rope is None:
+        raise ValueError("q needs a rope")
+    r = None
+    if rope is not None:
+        if rope.inv_freq.device != dev:
+            raise ValueError(f"inv_freq is on {rope.inv_freq.device}, the cache on {dev}")
+        axes = len(rope.sections)
+        if isinstance(positions, torch.Tensor) and positions.dim() == 1 and axes == 1:
+            positions = positions[None]
+        _kv_tensor(positions, "positions", torch.int32, (axes, rows), dev, strided=True)
+        r = RopeDesc.from_buffer_copy(rope.desc)
+        r.positions, r.axis_stride = positions.data_ptr(), positions.stride(0) if axes > 1 else 0
+    with _On(dev, stream) as on:
+        qr = orr = None
+        if q is not None:
+            _kv_tensor(q, "q", k.dtype, (rows, None, D), dev, strided=True)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            else:
+                _kv_tensor(q_out, "q_out", k.dtype, tuple(q.shape), dev, strided=True)
+            qr, orr = C.byref(_head_rows(q)), C.byref(_head_rows(q_out))
+        if rows:
+            _check(lib().tq_kv_append(cache.ref, ACT_TYPES[k.dtype], rows, slots.data_ptr(),
+                                      C.byref(_head_rows(k)), C.byref(_head_rows(v)), qr, orr,
+                                      None if r is None else C.byref(r), on.handle))
+    return q_out
+
+
+def kv_read(cache: KvCache, slots: torch.Tensor, dtype: torch.dtype = torch.float32, stream=None):
+    """The keys and values at `slots` (int32 [rows]) as the values they stand for, two tensors
+    [rows, kv_heads, head_dim] of `dtype` (tq_kv_read); zeros for slots outside the cache."""
+    dev = cache.device
+    _kv_tensor(slots, "slots", torch.int32, (None,), dev)
+    if dtype not in ACT_TYPES:
+        raise ValueError("dtype must be fp32, bf16 or fp16")
+    rows = slots.shape[0]
+    with _On(dev, stream) as on:
+        k = torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev)
+        v = torch.empty_like(k)
+        if rows:
+            _check(lib().tq_kv_read(cache.ref, ACT_TYPES[dtype], rows, slots.data_ptr(),
+                                    k.data_ptr(), v.data_ptr(), on.handle))
+    return k, v
+
+
+def kv_attention(cache: KvCache, q: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor,
+                 cu_new: torch.Tensor, scale: float | None = None, window: int = 0,
+                 out: torch.Tensor | None = None, return_lse: bool = False,
+                 ws: torch.Tensor | None = None, stream=None):
+    """Softmax attention of q [rows, heads, head_dim] over the cache (tq_kv_attention): rows
+    cu_new[r] .. cu_new[r + 1] are the last tokens of request r, whose seq_len[r] tokens (their
+    own included) lie in the pages block_table[r]. scale: default head_dim ** -0.5; window: tokens
+    a row sees, itself included (0: all). Returns out (q's type), or (out, lse) with lse fp32
+    [rows, heads]. Rows outside cu_new are left as they were in `out` (undefined in a new one)."""
+    dev, D, i32 = cache.device, cache.head_dim, torch.int32
+    if not isinstance(q, torch.Tensor) or q.dtype not in ACT_TYPES:
+        raise ValueError("q must be a tensor of fp32, bf16 or fp16")
+    _kv_tensor(q, "q", q.dtype, (None, None, D), dev, strided=True)
+    rows, heads, _ = q.shape
+    if heads == 0 or heads % cache.kv_heads:
+        raise ValueError(f"{heads} heads of q are no multiple of the cache's {cache.kv_heads}")
+    _kv_tensor(seq_len, "seq_len", i32, (None,), dev)
+    R = seq_len.shape[0]
+    _kv_tensor(block_table, "block_table", i32, (R, None), dev)
+    _kv_tensor(cu_new, "cu_new", i32, (R + 1,), dev)
+    t = ACT_TYPES[q.dtype]
+    with _On(dev, stream) as on:
+        if out is None:
+            out = torch.empty((rows, heads, D), dtype=q.dtype, device=dev)
+        else:
+            _kv_tensor(out, "out", q.dtype, (rows, heads, D), dev, strided=True)
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
+        d = KvAttnDesc(rows, R, block_table.shape[1], _head_rows(q), _head_rows(out), _ptr(lse),
+                       block_table.data_ptr(), seq_len.data_ptr(), cu_new.data_ptr(),
+                       D ** -0.5 if scale is None else scale, window)
+        ref = C.byref(d)
+        if ws is None:  # of the calling stream: calls on other streams, and graphs, have their own
+            ws = torch.empty(int(lib().tq_kv_attention_workspace_bytes(cache.ref, t, ref)),
+                             dtype=torch.uint8, device=dev)
+        _check(lib().tq_kv_attention(cache.ref, t, ref, ws.data_ptr() or None,
+                                     ws.numel() * ws.element_size(), on.handle))
+    return (out, lse) if return_lse else out
 
 
 # Tuning knobs (TQ_KNOB_* of tq.h), for tests and tuning sweeps: the defaults are the production

@@ -12,6 +12,7 @@
 
 #include "tq.h"
 #include "tq_chain.h"
+#include "tq_kv.h"
 #include "tq_launch.h"
 #include "tq_moe.h"
 
@@ -881,6 +882,262 @@ int tq_chain_status(void *plan, void *stream) {
   return fail(TQ_EDEVICE, "tq_chain_status: a run gave up waiting %s at op %u (the chain's "
                           "workgroups were not all resident, or the device stalled); its outputs "
                           "are undefined", kinds[kind < 5 ? kind : 0], word & 0xFFFFFFu);
+}
+
+// ---- the paged 4-bit key/value cache --------------------------------------------------------------
+
+namespace {
+
+bool kv_type(int t) { return t == TQ_F32 || t == TQ_BF16 || t == TQ_F16; }
+int64_t kv_type_bytes(int t) { return t == TQ_F32 ? 4 : 2; }
+
+bool kv_shape_ok(const tq_kv_cache *c) {
+  const bool page = c->page_tokens >= 16 && c->page_tokens <= 1024 && (c->page_tokens & (c->page_tokens - 1)) == 0;
+  const bool dim = c->head_dim == 64 || c->head_dim == 96 || c->head_dim == 128 || c->head_dim == 256;
+  return page && dim && c->kv_heads >= 1 && c->kv_heads <= 1024;
+}
+
+int kv_check(const char *what, const tq_kv_cache *c, bool data) {
+  if (!c) return fail(TQ_EINVAL, "%s: null cache", what);
+  if (!kv_shape_ok(c))
+    return fail(TQ_ESHAPE, "%s: kv_heads=%lld head_dim=%lld page_tokens=%lld (need 1..1024 heads of 64, 96, 128 "
+                "or 256, pages of 16, 32, ... 1024 tokens)", what, (long long)c->kv_heads, (long long)c->head_dim,
+                (long long)c->page_tokens);
+  if (c->pages < 1 || c->pages >= ((int64_t)1 << 31) / c->page_tokens)
+    return fail(TQ_ESHAPE, "%s: pages=%lld (need 1 <= pages and pages * page_tokens < 2^31)", what, (long long)c->pages);
+  if (data && !c->data) return fail(TQ_EINVAL, "%s: null cache data", what);
+  if (data && !aligned(c->data, 16)) return fail(TQ_EALIGN, "%s: cache data must be 16-byte aligned", what);
+  return TQ_OK;
+}
+
+// Rows of heads: a head's values are dense, so an output's heads (and rows) must lie apart by at
+// least a head (a row); inputs may repeat (stride 0).
+int kv_rows_check(const char *what, const char *name, const tq_head_rows *h, int type, int64_t head_dim, int64_t rows,
+                  bool output) {
+  const int64_t far = (int64_t)1 << 40;
+  if (!h || !h->data) return fail(TQ_EINVAL, "%s: null %s", what, name);
+  if (h->row_stride < 0 || h->head_stride < 0 || h->row_stride > far || h->head_stride > far)
+    return fail(TQ_ESHAPE, "%s: %s strides %lld, %lld", what, name, (long long)h->row_stride, (long long)h->head_stride);
+  if (output) {
+    const int64_t r = h->row_stride, s = h->head_stride, n = h->heads;
+    const bool heads_in_rows = (n == 1 || s >= head_dim) && (rows <= 1 || r >= (n - 1) * s + head_dim);
+    const bool rows_in_heads = (rows <= 1 || r >= head_dim) && (n == 1 || s >= (rows - 1) * r + head_dim);
+    if (!heads_in_rows && !rows_in_heads)
+      return fail(TQ_ESHAPE, "%s: rows or heads of %s overlap (strides %lld, %lld)", what, name, (long long)r, (long long)s);
+  }
+  if (!aligned(h->data, (uintptr_t)kv_type_bytes(type))) return fail(TQ_EALIGN, "%s: %s not aligned to its type", what, name);
+  return TQ_OK;
+}
+
+tq::HeadRows kv_rows(const tq_head_rows *h) {
+  tq::HeadRows r{};
+  if (h && h->data) {
+    r.data = h->data;
+    r.row_stride = h->row_stride;
+    r.head_stride = h->head_stride;
+    r.heads = (int)h->heads;
+  }
+  return r;
+}
+
+constexpr int64_t kKvMaxRows = (int64_t)1 << 20;
+
+// The arguments of tq_kv_attention (pointers only with `pointers`) as the kernels take them.
+int kv_attn_check(const tq_kv_cache *c, int type, const tq_kv_attn *t, bool pointers, tq::AttnArgs *out) {
+  const char *what = "tq_kv_attention";
+  int rc = kv_check(what, c, pointers);
+  if (rc != TQ_OK) return rc;
+  if (!t) return fail(TQ_EINVAL, "%s: null arguments", what);
+  if (!kv_type(type)) return fail(TQ_EINVAL, "%s: unknown type %d", what, type);
+  if (t->rows < 0 || t->rows > kKvMaxRows || t->requests < 1 || t->requests > 4096)
+    return fail(TQ_ESHAPE, "%s: rows=%lld requests=%lld (need 0..2^20, 1..4096)", what, (long long)t->rows,
+                (long long)t->requests);
+  if (t->max_blocks < 1 || t->max_blocks > ((int64_t)1 << 30) / c->page_tokens)
+    return fail(TQ_ESHAPE, "%s: max_blocks=%lld (need 1.. with max_blocks * page_tokens <= 2^30)", what,
+                (long long)t->max_blocks);
+  if (t->q.heads < 1 || t->q.heads > 4096 || t->q.heads % c->kv_heads || t->out.heads != t->q.heads)
+    return fail(TQ_ESHAPE, "%s: %lld q heads, %lld output heads (need a multiple of kv_heads=%lld up to 4096, the same)",
+                what, (long long)t->q.heads, (long long)t->out.heads, (long long)c->kv_heads);
+  if (t->window < 0 || t->window >= ((int64_t)1 << 31)) return fail(TQ_ESHAPE, "%s: window=%lld", what, (long long)t->window);
+  if (!(t->scale > 0.f && t->scale <= 3.4028235e38f)) return fail(TQ_EINVAL, "%s: scale must be positive and finite", what);
+  if (pointers && t->rows > 0) {
+    if ((rc = kv_rows_check(what, "q", &t->q, type, c->head_dim, t->rows, false)) != TQ_OK) return rc;
+    if ((rc = kv_rows_check(what, "out", &t->out, type, c->head_dim, t->rows, true)) != TQ_OK) return rc;
+    if (!t->block_table || !t->seq_len || !t->cu_new) return fail(TQ_EINVAL, "%s: null block_table, seq_len or cu_new", what);
+    if (!aligned(t->block_table, 4) || !aligned(t->seq_len, 4) || !aligned(t->cu_new, 4) || !aligned(t->lse, 4))
+      return fail(TQ_EALIGN, "%s: block_table, seq_len, cu_new and lse must be 4-byte aligned", what);
+  }
+  tq::AttnArgs a{};
+  a.g = tq::kv_geom(*c);
+  a.rows = (int)t->rows;
+  a.requests = (int)t->requests;
+  a.max_blocks = (int)t->max_blocks;
+  a.group = (int)(t->q.heads / c->kv_heads);
+  a.window = (int)t->window;
+  a.scale = (float)((double)t->scale * 1.4426950408889634);
+  a.q = kv_rows(&t->q);
+  a.out = kv_rows(&t->out);
+  a.lse = t->lse;
+  a.block_table = t->block_table;
+  a.seq_len = t->seq_len;
+  a.cu_new = t->cu_new;
+  a.grid = tq::kv_attention_grid(type, c->kv_heads, c->head_dim, a.group, t->rows, t->requests, t->max_blocks * c->page_tokens);
+  *out = a;
+  return TQ_OK;
+}
+
+}  // namespace
+
+size_t tq_kv_page_bytes(const tq_kv_cache *c) {
+  return c && kv_shape_ok(c) ? (size_t)tq::kv_geom(*c).page_bytes : 0;
+}
+
+int tq_kv_plan(const tq_kv_cache *c, const tq_kv_step *t, void *stream) {
+  int rc = kv_check("tq_kv_plan", c, false);
+  if (rc != TQ_OK) return rc;
+  if (!t) return fail(TQ_EINVAL, "tq_kv_plan: null step");
+  if (t->requests < 1 || t->requests > 4096 || t->rows < 0 || t->rows >= ((int64_t)1 << 28) || t->max_blocks < 1 ||
+      t->max_blocks > ((int64_t)1 << 30) / c->page_tokens)
+    return fail(TQ_ESHAPE, "tq_kv_plan: requests=%lld rows=%lld max_blocks=%lld (need 1..4096, 0..2^28 - 1, 1.. with "
+                "max_blocks * page_tokens <= 2^30)", (long long)t->requests, (long long)t->rows, (long long)t->max_blocks);
+  const void *need[] = {t->kv_len, t->new_len, t->block_table, t->cu_new, t->seq_len, t->status};
+  const void *per_row[] = {t->slots, t->positions, t->requests_of};
+  const void *managed[] = {t->free_count, t->free_count_out};
+  const void *all[] = {t->kv_len, t->new_len, t->block_table, t->cu_new, t->seq_len, t->status, t->slots, t->positions,
+                       t->requests_of, t->free_count, t->free_count_out, t->free_pages};
+  for (const void *p : need)
+    if (!p) return fail(TQ_EINVAL, "tq_kv_plan: null pointer");
+  for (const void *p : per_row)
+    if (!p && t->rows > 0) return fail(TQ_EINVAL, "tq_kv_plan: null slots, positions or requests_of");
+  for (const void *p : managed)
+    if (!p && t->free_pages) return fail(TQ_EINVAL, "tq_kv_plan: free_pages needs free_count and free_count_out");
+  for (const void *p : all)
+    if (!aligned(p, 4)) return fail(TQ_EALIGN, "tq_kv_plan: arrays must be 4-byte aligned");
+  for (size_t i = 0; i < sizeof all / sizeof *all; ++i)
+    for (size_t j = 0; j < i; ++j)
+      if (all[i] && all[i] == all[j]) return fail(TQ_EINVAL, "tq_kv_plan: two arrays are the same memory");
+  tq::PlanArgs a{};
+  a.requests = (int)t->requests;
+  a.max_blocks = (int)t->max_blocks;
+  a.rows = (int)t->rows;
+  a.page_shift = tq::kv_geom(*c).page_shift;
+  a.pages = (int)c->pages;
+  a.kv_len = t->kv_len;
+  a.new_len = t->new_len;
+  a.block_table = t->block_table;
+  a.free_pages = t->free_pages;
+  a.free_count = t->free_pages ? t->free_count : nullptr;
+  a.cu_new = t->cu_new;
+  a.seq_len = t->seq_len;
+  a.slots = t->slots;
+  a.positions = t->positions;
+  a.requests_of = t->requests_of;
+  a.free_count_out = t->free_pages ? t->free_count_out : nullptr;
+  a.status = t->status;
+  return launched(tq::launch_kv_plan(a, (hipStream_t)stream), "tq_kv_plan");
+}
+
+int tq_kv_append(const tq_kv_cache *c, int type, int64_t rows, const int32_t *slots, const tq_head_rows *k,
+                 const tq_head_rows *v, const tq_head_rows *q, const tq_head_rows *q_out, const tq_rope *rope,
+                 void *stream) {
+  const char *what = "tq_kv_append";
+  int rc = kv_check(what, c, rows != 0);
+  if (rc != TQ_OK) return rc;
+  if (!kv_type(type)) return fail(TQ_EINVAL, "%s: unknown type %d", what, type);
+  if (rows < 0 || rows > kKvMaxRows) return fail(TQ_ESHAPE, "%s: rows=%lld not in 0..2^20", what, (long long)rows);
+  if (rows == 0) return TQ_OK;
+  if (!slots) return fail(TQ_EINVAL, "%s: null slots", what);
+  if (!aligned(slots, 4)) return fail(TQ_EALIGN, "%s: slots must be 4-byte aligned", what);
+  if ((rc = kv_rows_check(what, "k", k, type, c->head_dim, rows, false)) != TQ_OK) return rc;
+  if ((rc = kv_rows_check(what, "v", v, type, c->head_dim, rows, false)) != TQ_OK) return rc;
+  if (k->heads != c->kv_heads || v->heads != c->kv_heads)
+    return fail(TQ_ESHAPE, "%s: k has %lld heads, v %lld, the cache %lld", what, (long long)k->heads, (long long)v->heads,
+                (long long)c->kv_heads);
+  const bool has_q = q && q->data, has_out = q_out && q_out->data;
+  if (has_q != has_out) return fail(TQ_EINVAL, "%s: q and q_out go together", what);
+  if (has_q) {
+    if (!rope) return fail(TQ_EINVAL, "%s: q needs a rope", what);
+    if (q->heads < 1 || q->heads > 4096 || q_out->heads != q->heads)
+      return fail(TQ_ESHAPE, "%s: %lld q heads, %lld output heads (need 1..4096, the same)", what, (long long)q->heads,
+                  (long long)q_out->heads);
+    if ((rc = kv_rows_check(what, "q", q, type, c->head_dim, rows, false)) != TQ_OK) return rc;
+    if ((rc = kv_rows_check(what, "q_out", q_out, type, c->head_dim, rows, true)) != TQ_OK) return rc;
+    if (q->data == q_out->data && (q->row_stride != q_out->row_stride || q->head_stride != q_out->head_stride))
+      return fail(TQ_EINVAL, "%s: q_out in q's memory needs q's strides", what);
+  }
+  tq::AppendArgs a{};
+  if (rope) {
+    if (!rope->inv_freq || !rope->positions) return fail(TQ_EINVAL, "%s: null inv_freq or positions", what);
+    if (!aligned(rope->inv_freq, 4) || !aligned(rope->positions, 4))
+      return fail(TQ_EALIGN, "%s: inv_freq and positions must be 4-byte aligned", what);
+    if (rope->pairs < 1 || 2 * rope->pairs > c->head_dim || rope->axes < 1 || rope->axes > 4)
+      return fail(TQ_ESHAPE, "%s: %lld pairs, %lld axes (need 1..head_dim/2, 1..4)", what, (long long)rope->pairs,
+                  (long long)rope->axes);
+    if (rope->axes > 1 && rope->axis_stride < 0) return fail(TQ_ESHAPE, "%s: negative axis_stride", what);
+    int64_t sum = 0;
+    for (int i = 0; i < 4; ++i) {
+      if (i < rope->axes) {
+        if (rope->sections[i] < 0 || rope->sections[i] > rope->pairs) return fail(TQ_ESHAPE, "%s: sections", what);
+        sum += rope->sections[i];
+      }
+      a.section_end[i] = (int)sum;
+    }
+    if (sum != rope->pairs) return fail(TQ_ESHAPE, "%s: the sections add up to %lld, not to %lld pairs", what, (long long)sum,
+                                        (long long)rope->pairs);
+    a.inv_freq = rope->inv_freq;
+    a.positions = rope->positions;
+    a.axis_stride = rope->axis_stride;
+    a.pairs = (int)rope->pairs;
+    a.interleaved = rope->interleaved != 0;
+  }
+  a.g = tq::kv_geom(*c);
+  a.rows = (int)rows;
+  a.head_dim = (int)c->head_dim;
+  a.slots = slots;
+  a.k = kv_rows(k);
+  a.v = kv_rows(v);
+  a.q = kv_rows(has_q ? q : nullptr);
+  a.q_out = kv_rows(has_q ? q_out : nullptr);
+  return launched(tq::launch_kv_append(type, a, (hipStream_t)stream), what);
+}
+
+int tq_kv_read(const tq_kv_cache *c, int type, int64_t rows, const int32_t *slots, void *k, void *v, void *stream) {
+  const char *what = "tq_kv_read";
+  const int rc = kv_check(what, c, rows != 0);
+  if (rc != TQ_OK) return rc;
+  if (!kv_type(type)) return fail(TQ_EINVAL, "%s: unknown type %d", what, type);
+  if (rows < 0 || rows > kKvMaxRows) return fail(TQ_ESHAPE, "%s: rows=%lld not in 0..2^20", what, (long long)rows);
+  if (rows == 0 || (!k && !v)) return TQ_OK;
+  if (!slots) return fail(TQ_EINVAL, "%s: null slots", what);
+  if (!aligned(slots, 4) || !aligned(k, 16) || !aligned(v, 16))
+    return fail(TQ_EALIGN, "%s: slots must be 4-byte, k and v 16-byte aligned", what);
+  tq::ReadArgs a{};
+  a.g = tq::kv_geom(*c);
+  a.rows = (int)rows;
+  a.head_dim = (int)c->head_dim;
+  a.slots = slots;
+  a.k = k;
+  a.v = v;
+  return launched(tq::launch_kv_read(type, a, (hipStream_t)stream), what);
+}
+
+size_t tq_kv_attention_workspace_bytes(const tq_kv_cache *c, int type, const tq_kv_attn *t) {
+  tq::AttnArgs a;
+  if (kv_attn_check(c, type, t, false, &a) != TQ_OK) return 0;
+  return tq::kv_attention_workspace(type, c->head_dim, a.grid);
+}
+
+int tq_kv_attention(const tq_kv_cache *c, int type, const tq_kv_attn *t, void *workspace, size_t ws_bytes, void *stream) {
+  tq::AttnArgs a;
+  const int rc = kv_attn_check(c, type, t, true, &a);
+  if (rc != TQ_OK) return rc;
+  if (a.rows == 0) return TQ_OK;
+  const size_t need = tq::kv_attention_workspace(type, c->head_dim, a.grid);
+  if (!workspace) return fail(TQ_EINVAL, "tq_kv_attention: null workspace");
+  if (!aligned(workspace, 256)) return fail(TQ_EALIGN, "tq_kv_attention: workspace must be 256-byte aligned");
+  if (ws_bytes < need) return fail(TQ_ENOSPC, "tq_kv_attention: workspace of %zu bytes, %zu needed", ws_bytes, need);
+  a.parts = (float *)workspace;
+  return launched(tq::launch_kv_attention(type, a, (hipStream_t)stream), "tq_kv_attention");
 }
 
 }  // extern "C"

@@ -1,0 +1,425 @@
+// tq_kv.hip -- the step plan, the append and the read-back of the paged 4-bit key/value cache.
+#include "tq_kv.h"
+#include "tq_kv_device.h"
+#include "tq_launch.h"
+
+namespace tq {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+int launch_status() { return hipGetLastError() == hipSuccess ? 0 : -1; }
+
+// ---- plan -----------------------------------------------------------------------------------
+
+// Index of the run that holds i: off[0] <= ... <= off[n], off[r] <= i < off[r + 1].
+__device__ __forceinline__ int run_of(const int32_t *off, int n, int i) {
+  int lo = 0, hi = n;  // first index > i lies in (lo, hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Prefix sums over the requests of new tokens, needed pages and released pages; then every row,
+// needed page and released page finds its request by bisection. Bound by latency (two dependent
+// reads, the scan's barriers, the bisection): each workgroup repeats the scan of at most 4096
+// requests from L2 rather than wait for another one's, so a step is a single launch. Nothing reads
+// what another workgroup of the launch writes: pages on the stack above free_count are read from
+// the ended requests' table rows, which the launch leaves alone.
+__global__ __launch_bounds__(kThreads) void k_kv_plan(PlanArgs a) {
+  extern __shared__ int32_t plan_lds[];
+  __shared__ int64_t wave_sum[3][kThreads / 64];
+  __shared__ int bad_lds;
+  const int R = a.requests, tid = threadIdx.x, lane = tid & 63, wave = wave_index();
+  int32_t *cu = plan_lds, *need = cu + R + 1, *rel = need + R + 1;
+  const int P = 1 << a.page_shift;
+  const bool managed = a.free_pages != nullptr;
+  if (tid == 0) bad_lds = 0;
+  const int per = (R + kThreads - 1) / kThreads, r0 = min(R, tid * per), r1 = min(R, r0 + per);
+  int64_t s[3] = {0, 0, 0};
+  int bad = 0;
+  auto request = [&](int r, int64_t v[3]) {
+    const int kv = a.kv_len[r], nw = a.new_len[r];
+    v[0] = v[1] = v[2] = 0;
+    if (kv < 0 || nw < -1) {
+      bad |= 8;
+      return;
+    }
+    const int64_t have = ((int64_t)kv + P - 1) >> a.page_shift;
+    const int64_t after = ((int64_t)kv + max(nw, 0) + P - 1) >> a.page_shift;
+    if (after > a.max_blocks) bad |= 4;
+    if (nw < 0) {
+      v[2] = managed ? have : 0;
+    } else {
+      v[0] = nw;
+      v[1] = managed ? after - have : 0;
+    }
+  };
+  for (int r = r0; r < r1; ++r) {
+    int64_t v[3];
+    request(r, v);
+    for (int i = 0; i < 3; ++i) s[i] += v[i];
+  }
+  int64_t incl[3];
+  for (int i = 0; i < 3; ++i) {
+    int64_t x = s[i];
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t y = __shfl_up(x, d);
+      if (lane >= d) x += y;
+    }
+    incl[i] = x;
+    if (lane == 63) wave_sum[i][wave] = x;
+  }
+  __syncthreads();
+  int64_t total[3], base[3];
+  for (int i = 0; i < 3; ++i) {
+    total[i] = 0;
+    base[i] = incl[i] - s[i];
+    for (int w = 0; w < kThreads / 64; ++w) {
+      if (w < wave) base[i] += wave_sum[i][w];
+      total[i] += wave_sum[i][w];
+    }
+  }
+  const int64_t fc = managed ? a.free_count[0] : 0;
+  if (managed && (fc < 0 || fc > a.pages || fc + total[2] > a.pages)) bad |= 8;
+  else if (managed && total[1] > fc + total[2]) bad |= 1;
+  if (total[0] > a.rows) bad |= 2;
+  if (bad) atomicOr(&bad_lds, bad);
+  __syncthreads();
+  bad = bad_lds;
+  const int first = blockIdx.x * kThreads + tid, step = gridDim.x * kThreads;
+  if (first == 0) {
+    a.status[0] = bad;
+    if (a.free_count_out) a.free_count_out[0] = (int32_t)(bad ? (managed ? a.free_count[0] : 0) : fc + total[2] - total[1]);
+  }
+  if (bad) {
+    for (int r = first; r <= R; r += step) {
+      a.cu_new[r] = 0;
+      if (r < R) a.seq_len[r] = max(a.kv_len[r], 0);
+    }
+    for (int t = first; t < a.rows; t += step) a.slots[t] = a.positions[t] = a.requests_of[t] = -1;
+    return;
+  }
+  for (int r = r0; r < r1; ++r) {
+    cu[r] = (int32_t)base[0];
+    need[r] = (int32_t)base[1];
+    rel[r] = (int32_t)base[2];
+    int64_t v[3];
+    request(r, v);
+    for (int i = 0; i < 3; ++i) base[i] += v[i];
+  }
+  if (tid == 0) {
+    cu[R] = (int32_t)total[0];
+    need[R] = (int32_t)total[1];
+    rel[R] = (int32_t)total[2];
+  }
+  __syncthreads();
+  auto have_of = [&](int r) { return (int)(((int64_t)a.kv_len[r] + P - 1) >> a.page_shift); };
+  auto stack = [&](int i) -> int32_t {  // 0 <= i < fc + total[2]
+    if (i < fc) return a.free_pages[i];
+    i -= (int)fc;
+    const int r = run_of(rel, R, i);
+    return a.block_table[(int64_t)r * a.max_blocks + (i - rel[r])];
+  };
+  const int top = (int)(fc + total[2]);
+  for (int r = first; r <= R; r += step) {
+    a.cu_new[r] = cu[r];
+    if (r < R) {
+      const int nw = a.new_len[r];
+      a.seq_len[r] = nw < 0 ? 0 : a.kv_len[r] + nw;
+    }
+  }
+  for (int t = first; t < a.rows; t += step) {
+    int slot = -1, pos = -1, r = -1;
+    if (t < cu[R]) {
+      r = run_of(cu, R, t);
+      const int kv = a.kv_len[r];
+      pos = kv + (t - cu[r]);
+      const int col = pos >> a.page_shift, have = (int)(((int64_t)kv + P - 1) >> a.page_shift);
+      const int32_t page = managed && col >= have ? stack(top - 1 - (need[r] + col - have))
+                                                  : a.block_table[(int64_t)r * a.max_blocks + col];
+      if (page >= 0 && page < a.pages) slot = (page << a.page_shift) + (pos & (P - 1));
+    }
+    a.slots[t] = slot;
+    a.positions[t] = pos;
+    a.requests_of[t] = r;
+  }
+  for (int j = first; j < need[R]; j += step) {
+    const int r = run_of(need, R, j);
+    a.block_table[(int64_t)r * a.max_blocks + have_of(r) + (j - need[r])] = stack(top - 1 - j);
+  }
+  for (int j = first; j < rel[R]; j += step) a.free_pages[fc + j] = stack((int)fc + j);
+}
+
+// ---- append ---------------------------------------------------------------------------------
+
+// One workgroup: `rb` rows x `hg` kv heads (and their share of the q heads). The rows' sines and
+// cosines are formed once per workgroup in fp64 (an fp32 angle is off by 0.03 rad at position
+// 500000) and kept in LDS; q heads go from global memory to global memory, k and v heads into LDS
+// as fp32, from where sixteen lanes round a block of 32 (lane c holds its values c and c + 16, the
+// two nibbles of one byte). W pairs are turned per thread step.
+template <typename A, int W>
+__global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a, int rb, int hg) {
+  typedef typename A::type T;
+  extern __shared__ double2 append_lds[];
+  __shared__ int slot_lds[16];
+  const int tid = threadIdx.x, D = a.head_dim, pairs = a.inv_freq ? a.pairs : 0;
+  const int row0 = blockIdx.x * rb, rows = min(rb, a.rows - row0);
+  const int h0 = blockIdx.y * hg, heads = min(hg, a.g.heads - h0);
+  const int q0 = (int)((int64_t)a.q.heads * blockIdx.y / gridDim.y);
+  const int qn = (int)((int64_t)a.q.heads * (blockIdx.y + 1) / gridDim.y) - q0;
+  double2 *turn = append_lds;                                // [rb][pairs]: cosine, sine
+  float *stage = (float *)(append_lds + (int64_t)rb * pairs);  // [rb][k heads, v heads][D]
+  if (tid < rows) {
+    const int slot = a.slots[row0 + tid];
+    slot_lds[tid] = slot >= 0 && (slot >> a.g.page_shift) < a.g.pages ? slot : -1;
+  }
+  __syncthreads();
+  for (int i = tid; i < rows * pairs; i += kThreads) {
+    const int row = i / pairs, p = i - row * pairs;
+    if (slot_lds[row] < 0) continue;
+    int axis = 0;
+    while (axis < 3 && p >= a.section_end[axis]) ++axis;
+    const double angle = (double)a.positions[axis * a.axis_stride + row0 + row] * (double)a.inv_freq[p];
+    double si, co;
+    sincos(angle, &si, &co);
+    turn[i] = make_double2(co, si);
+  }
+  __syncthreads();
+  const int units = D / (2 * W);  // thread steps per head
+  const int per_row = qn + 2 * heads;
+  for (int i = tid; i < rows * per_row * units; i += kThreads) {
+    const int u = i % units, rest = i / units, row = rest / per_row, j = rest - row * per_row;
+    if (slot_lds[row] < 0) continue;
+    const bool is_q = j < qn, is_v = j >= qn + heads;
+    const int head = is_q ? q0 + j : h0 + j - qn - (is_v ? heads : 0);
+    const T *x = (const T *)(is_q ? a.q.data : is_v ? a.v.data : a.k.data) +
+                 (row0 + row) * (is_q ? a.q.row_stride : is_v ? a.v.row_stride : a.k.row_stride) +
+                 head * (is_q ? a.q.head_stride : is_v ? a.v.head_stride : a.k.head_stride);
+    // the two runs of W elements that this step takes, W pairs or 2 W elements that stay
+    const bool turned = !is_v && u * W < pairs;
+    int e0, e1;
+    if (turned && !a.interleaved) {
+      e0 = u * W;
+      e1 = e0 + pairs;
+    } else if (!is_v && !turned) {  // past the turned ones
+      e0 = 2 * pairs + (u * W - pairs) * 2;
+      e1 = e0 + W;
+    } else {
+      e0 = 2 * u * W;
+      e1 = e0 + W;
+    }
+    float lo[W], hi[W];
+    load_run<A, W, (W > 1)>(x + e0, lo);
+    load_run<A, W, (W > 1)>(x + e1, hi);
+    double dlo[W], dhi[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      dlo[k] = lo[k];
+      dhi[k] = hi[k];
+    }
+    if (turned) {
+      const double2 *t = turn + row * pairs + u * W;
+      if (a.interleaved) {
+        double v[2 * W];
+#pragma unroll
+        for (int k = 0; k < 2 * W; ++k) v[k] = k < W ? dlo[k] : dhi[k - W];
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          const double x0 = v[2 * k], x1 = v[2 * k + 1], c = t[k].x, s = t[k].y;
+          v[2 * k] = x0 * c - x1 * s;
+          v[2 * k + 1] = x0 * s + x1 * c;
+        }
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          dlo[k] = v[k];
+          dhi[k] = v[W + k];
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          const double x0 = dlo[k], x1 = dhi[k], c = t[k].x, s = t[k].y;
+          dlo[k] = x0 * c - x1 * s;
+          dhi[k] = x0 * s + x1 * c;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      lo[k] = (float)dlo[k];
+      hi[k] = (float)dhi[k];
+    }
+    if (is_q) {
+      T *y = (T *)a.q_out.data + (row0 + row) * a.q_out.row_stride + head * a.q_out.head_stride;
+      store_run<A, W, (W > 1)>(y + e0, lo);
+      store_run<A, W, (W > 1)>(y + e1, hi);
+    } else {
+      float *y = stage + ((int64_t)row * 2 * heads + (j - qn)) * D;
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        y[e0 + k] = lo[k];
+        y[e1 + k] = hi[k];
+      }
+    }
+  }
+  __syncthreads();
+  const int nb = a.g.nb, blocks = rows * 2 * heads * nb;
+  const int lane = tid & 63, c = lane & 15, wave = wave_index();
+  for (int i0 = wave * 4; i0 < blocks; i0 += kThreads / 16) {
+    const int i = min(i0 + (lane >> 4), blocks - 1);  // the ballots below take whole waves
+    const int b = i % nb, rest = i / nb, j = rest % (2 * heads), row = rest / (2 * heads);
+    const int slot = slot_lds[row];
+    const bool live = slot >= 0 && i == i0 + (lane >> 4);
+    const float *x = stage + ((int64_t)row * 2 * heads + j) * D + 32 * b;
+    const float lo = slot >= 0 ? x[c] : 0.f, hi = slot >= 0 ? x[c + 16] : 0.f;
+    const bool odd = !(fabsf(lo) < INFINITY) || !(fabsf(hi) < INFINITY);
+    float most = fmaxf(fabsf(lo), fabsf(hi));
+    for (int d = 1; d < 16; d <<= 1) most = fmaxf(most, __shfl_xor(most, d));
+    const int sh = lane & 48;
+    auto group = [&](bool v) { return (unsigned)(__ballot(v) >> sh) & 0xFFFFu; };
+    const unsigned in_lo = group(fabsf(lo) == most), in_hi = group(fabsf(hi) == most);
+    const unsigned neg_lo = group(lo < 0.f), neg_hi = group(hi < 0.f), any_odd = group(odd);
+    // sign of the first value of largest magnitude: values 0..15 are the lo ones
+    const bool negative = in_lo ? (neg_lo >> __builtin_ctz(in_lo)) & 1
+                                : in_hi ? (neg_hi >> __builtin_ctz(in_hi)) & 1 : false;
+    const float want = fminf(most * 0.125f, 65504.f);
+    _Float16 d = (_Float16)(negative ? want : -want);
+    if (any_odd) d = __builtin_bit_cast(_Float16, (uint16_t)0x7E00);
+    const float df = (float)d, inv = 1.f / df;
+    // nearest even of v / d, exactly: v - n d is exact in fp32 (n has 4 bits, d 11), so its
+    // comparison with d / 2 settles what the rounded reciprocal may have missed
+    auto nibble = [&](float v) -> uint32_t {
+      if (any_odd || df == 0.f) return 8u;
+      float n = fminf(fmaxf(rintf(v * inv), -9.f), 9.f);
+      const float r = fmaf(-n, df, v), h = 0.5f * fabsf(df);
+      const float toward = (r < 0.f) == (df < 0.f) ? 1.f : -1.f;  // the neighbour on r's side
+      const float m = n + toward;
+      if (fabsf(r) > h || (fabsf(r) == h && ((int)n & 1))) n = m;
+      return (uint32_t)(8 + (int)fminf(fmaxf(n, -8.f), 7.f));
+    };
+    const uint32_t byte = nibble(lo) | nibble(hi) << 4;
+    const int h = h0 + (j < heads ? j : j - heads), tok = slot & 15;
+    const bool is_v = j >= heads;
+    uint8_t *tile = a.g.data + (slot >= 0 ? tile_of_slot(a.g, slot, h) : 0) + (is_v ? a.g.half_bytes : 0);
+    uint32_t word = byte << (8 * quant_place(c));
+    word |= __shfl_xor(word, 1);
+    word |= __shfl_xor(word, 2);
+    if (!live) continue;
+    if (!is_v) {
+      if ((c & 3) == 0) ((uint32_t *)tile)[quant_word(a.g, b, c >> 2, tok)] = word;
+    } else {
+      tile[4 * quant_word(a.g, b, tok >> 2, c) + quant_place(tok)] = (uint8_t)byte;
+    }
+    if (c == 0) ((_Float16 *)(tile + a.g.quant_bytes))[((tok >> 2) * nb + b) * 4 + (tok & 3)] = d;
+  }
+}
+
+// ---- read -----------------------------------------------------------------------------------
+
+// One thread: four neighbouring values of each half of a block (one dword of key quants, or one
+// byte from each of four dwords of value quants).
+template <typename A>
+__global__ __launch_bounds__(kThreads) void k_kv_read(ReadArgs a) {
+  typedef typename A::type T;
+  const int nb = a.g.nb, per_head = nb * 4;
+  const int64_t per_row = (int64_t)a.g.heads * per_head, n = a.rows * per_row;
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;
+  const int row = (int)(i / per_row), in = (int)(i - row * per_row);
+  const int h = in / per_head, u = in - h * per_head, b = u >> 2, f = u & 3;
+  const int slot = a.slots[row];
+  const bool there = slot >= 0 && (slot >> a.g.page_shift) < a.g.pages;
+  const uint8_t *tile = a.g.data + (there ? tile_of_slot(a.g, slot, h) : 0);
+  const int tok = slot & 15, scale_at = ((tok >> 2) * nb + b) * 4 + (tok & 3);
+  const int64_t out = ((int64_t)row * a.g.heads + h) * a.head_dim + 32 * b + 4 * f;
+  auto give = [&](void *dst, const uint32_t byte[4], float d) {
+    float lo[4], hi[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      lo[k] = there ? d * (float)((int)(byte[k] & 15u) - 8) : 0.f;
+      hi[k] = there ? d * (float)((int)(byte[k] >> 4) - 8) : 0.f;
+    }
+    store_run<A, 4, true>((T *)dst + out, lo);
+    store_run<A, 4, true>((T *)dst + out + 16, hi);
+  };
+  if (a.k) {
+    uint32_t byte[4] = {0, 0, 0, 0};
+    float d = 0.f;
+    if (there) {
+      const uint32_t w = ((const uint32_t *)tile)[quant_word(a.g, b, f, tok)];
+      d = (float)((const _Float16 *)(tile + a.g.quant_bytes))[scale_at];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) byte[k] = (w >> (8 * quant_place(k))) & 0xFFu;
+    }
+    give(a.k, byte, d);
+  }
+  if (a.v) {
+    uint32_t byte[4] = {0, 0, 0, 0};
+    float d = 0.f;
+    if (there) {
+      tile += a.g.half_bytes;
+      d = (float)((const _Float16 *)(tile + a.g.quant_bytes))[scale_at];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        byte[k] = tile[4 * quant_word(a.g, b, tok >> 2, 4 * f + k) + quant_place(tok)];
+    }
+    give(a.v, byte, d);
+  }
+}
+
+template <typename A>
+int launch_append(const AppendArgs &a, hipStream_t s) {
+  const int pairs = a.inv_freq ? a.pairs : 0;
+  // few rows: one row and head per workgroup (latency); many: four rows share the sines of eight
+  // heads, within 60 KB of LDS
+  int rb = 1, hg = 1;
+  if ((int64_t)a.rows * a.g.heads > 1024) {
+    rb = 4;
+    hg = 8;
+    while (hg > 1 && rb * (pairs * 16 + 2 * hg * a.head_dim * 4) > 60 * 1024) hg >>= 1;
+  }
+  hg = hg < a.g.heads ? hg : a.g.heads;
+  const size_t lds = (size_t)rb * (pairs * 16 + 2 * hg * a.head_dim * 4);
+  const dim3 grid((a.rows + rb - 1) / rb, (a.g.heads + hg - 1) / hg);
+  auto fits = [](const HeadRows &h) {
+    return h.data == nullptr || (((uintptr_t)h.data % (4 * sizeof(typename A::type))) == 0 &&
+                                 h.row_stride % 4 == 0 && h.head_stride % 4 == 0);
+  };
+  if (pairs % 4 == 0 && fits(a.k) && fits(a.v) && fits(a.q) && fits(a.q_out))
+    k_kv_append<A, 4><<<grid, kThreads, lds, s>>>(a, rb, hg);
+  else
+    k_kv_append<A, 1><<<grid, kThreads, lds, s>>>(a, rb, hg);
+  return launch_status();
+}
+
+template <typename A>
+int launch_read(const ReadArgs &a, hipStream_t s) {
+  const int64_t n = (int64_t)a.rows * a.g.heads * a.g.nb * 4;
+  k_kv_read<A><<<dim3((unsigned)((n + kThreads - 1) / kThreads)), kThreads, 0, s>>>(a);
+  return launch_status();
+}
+
+}  // namespace
+
+int launch_kv_plan(const PlanArgs &a, hipStream_t s) {
+  const int work = a.rows > a.requests ? a.rows : a.requests;
+  const int grid = clampi((work + 2 * kThreads - 1) / (2 * kThreads), 1, 64);
+  k_kv_plan<<<dim3(grid), kThreads, (size_t)3 * (a.requests + 1) * 4, s>>>(a);
+  return launch_status();
+}
+
+int launch_kv_append(int type, const AppendArgs &a, hipStream_t s) {
+  return type == TQ_F32 ? launch_append<ActF32>(a, s)
+         : type == TQ_BF16 ? launch_append<ActBF16>(a, s) : launch_append<ActF16>(a, s);
+}
+
+int launch_kv_read(int type, const ReadArgs &a, hipStream_t s) {
+  return type == TQ_F32 ? launch_read<ActF32>(a, s)
+         : type == TQ_BF16 ? launch_read<ActBF16>(a, s) : launch_read<ActF16>(a, s);
+}
+
+}  // namespace tq
