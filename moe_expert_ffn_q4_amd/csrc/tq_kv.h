@@ -90,6 +90,7 @@ struct AttnArgs {
   float *lse;     // [rows][q heads] or null
   const int32_t *block_table, *seq_len, *cu_new;
   float *parts;   // partial results (workspace)
+  void *joins;    // behind them: the items to join
 };
 
 // Each returns 0 when everything was enqueued, -1 on a HIP launch error. `type` is TQ_F32,

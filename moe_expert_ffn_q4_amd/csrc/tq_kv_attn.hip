@@ -12,6 +12,7 @@
 #include "tq_kv.h"
 #include "tq_kv_device.h"
 #include "tq_launch.h"
+#include "tq_mfma.h"
 
 namespace tq {
 
@@ -20,24 +21,40 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x2a4 __attribute__((ext_vector_type(2), aligned(4)));
 typedef uint32_t u32x3a4 __attribute__((ext_vector_type(3), aligned(4)));
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kGrid = 512;       // workgroups of a full launch: two per compute unit
-constexpr int kMinSteps = 4;     // key steps (32 tokens) per workgroup at least: one per wave
+#ifndef KV_GRID
+#define KV_GRID 768
+#endif
+#ifndef KV_AHEAD4
+#define KV_AHEAD4 1
+#endif
+#ifndef KV_OCC
+#define KV_OCC 3
+#endif
+constexpr int kGrid = KV_GRID;      // workgroups of a full launch: four per compute unit
+#ifndef KV_ITEM
+#define KV_ITEM 8
+#endif
+#ifndef KV_MIN
+#define KV_MIN 8
+#endif
+constexpr int kMinUnits = KV_MIN;     // units per workgroup at least
+constexpr int kItemUnits = KV_ITEM;    // what an item costs beside its steps (queries, merge, output)
 constexpr float kLowest = -3.4028234663852886e38f;
-constexpr float kSlack = 7.f;    // see step()
+constexpr float kSlack = 2.f;    // see step()
 
 // ---- the step's work as one line of units -----------------------------------------------------
-// An item is a query tile (up to NCOL columns: tokens x heads of one kv head) of a request; the
-// units of an item are the 32-token steps of its request. All items' units form one line, cut
-// into equal shares, one a workgroup, so ragged batches load the chip evenly. The lengths live on
-// the device, so every workgroup forms the prefix sums over the requests itself.
+// An item is a query tile (up to NCOL columns: tokens x heads of one kv head) of a request; its
+// units are the 32-token steps of its request and kItemUnits for what it costs beside them. All
+// items' units form one line, cut into equal shares, one a workgroup, so ragged batches load the
+// chip evenly; a share of an item's units is the same share of its steps. The lengths live on the
+// device, so every workgroup forms the prefix sums over the requests itself.
 struct Request {
   int r, row0, fresh, len, first_pos;  // rows row0 .. row0 + fresh, tokens of the sequence
-  int tiles, steps;                    // query tiles, units per item
+  int tiles, units;                    // query tiles, units per item
 };
 
 struct TileShape {
@@ -64,12 +81,22 @@ __device__ __forceinline__ Request request(const AttnArgs &a, const TileShape &t
   q.len = (int)min((int64_t)max(a.seq_len[r], 0), (int64_t)a.max_blocks << a.g.page_shift);
   q.first_pos = q.len - q.fresh;
   q.tiles = (q.fresh + ts.tokens - 1) / ts.tokens * ts.splits;
-  q.steps = max(1, (q.len + 31) / 32 - seen_from(a, q.first_pos) / 32);
+  q.units = kItemUnits + max(0, (q.len + 31) / 32 - seen_from(a, q.first_pos) / 32);
   return q;
 }
 
 __device__ __forceinline__ int64_t units_of(const AttnArgs &a, const Request &q) {
-  return (int64_t)a.g.heads * q.tiles * q.steps;
+  return (int64_t)a.g.heads * q.tiles * q.units;
+}
+
+// a / b for 0 <= a < 2^53, 0 < b < 2^31 (a 64-bit integer division takes over a hundred
+// instructions; the quotient of the doubles is off by less than one).
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  int64_t q = (int64_t)((double)a / (double)b);
+  const int64_t r = a - q * b;
+  if (r < 0) --q;
+  if (r >= b) ++q;
+  return q;
 }
 
 struct Place {
@@ -77,6 +104,14 @@ struct Place {
   int r;               // the request that holds the wanted unit
   int64_t base;        // its first unit
 };
+
+// A value that is the same in all lanes, as a scalar (LDS reads are per lane to the compiler, and
+// everything derived from the place would then be computed per lane).
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
 
 // Called by every thread of the workgroup. `unit_of(per)`: the wanted unit.
 template <typename F>
@@ -103,7 +138,8 @@ __device__ __forceinline__ Place locate(const AttnArgs &a, const TileShape &ts, 
     if (w < wave) base += sums[w];
     p.total += sums[w];
   }
-  p.per = max((int64_t)kMinSteps, (p.total + a.grid - 1) / a.grid);
+  p.total = uniform64(p.total);
+  p.per = max((int64_t)kMinUnits, quotient(p.total + a.grid - 1, a.grid));
   const int64_t u = unit_of(p.per);
   if (u >= base && u < base + mine) {
     for (int r = r0; r < r1; ++r) {
@@ -117,52 +153,91 @@ __device__ __forceinline__ Place locate(const AttnArgs &a, const TileShape &ts, 
     }
   }
   __syncthreads();
-  p.r = (int)found[0];
-  p.base = found[1];
+  p.r = __builtin_amdgcn_readfirstlane((int)found[0]);
+  p.base = uniform64(found[1]);
   return p;
 }
 
 // ---- operands ---------------------------------------------------------------------------------
 
-// Four tokens (or dimensions) pairs of one dword of quants as fp16 integers n - 8:
-// low nibbles of bytes (0, 2), of bytes (1, 3), high nibbles of both pairs.
-__device__ __forceinline__ void unpack(uint32_t w, f16x2 out[4]) {
+// Constants of unpack(), in registers: with the masks as scalars and the exponent as a vector
+// register, mask and exponent are one v_and_or_b32 (an instruction takes one literal or scalar).
+struct Unpack {
+  uint32_t low, high, exponent;
+  __device__ __forceinline__ Unpack() : low(0x000F000Fu), high(0x00F000F0u), exponent(0x64006400u) {
+    asm("" : "+s"(low), "+s"(high), "+v"(exponent));
+  }
+};
+
+// The nibbles of one dword of quants as fp16 integers n - 8: the bits of a nibble under the exponent
+// of 1024 are 1024 + n, those of a high nibble 1024 + 16 n. Low nibbles of bytes (0, 2), of bytes
+// (1, 3), high nibbles of both pairs. (As fp16 subnormals n 2^-24, by masks alone, the products
+// lose up to ten bits: the matrix cores align a product by its operands' exponent fields. Measured
+// on this kernel: 3e-4 of the terms' magnitude against 3e-7.)
+__device__ __forceinline__ void unpack(const Unpack &k, uint32_t w, uint32_t out[4]) {
   const uint32_t u = w >> 8;
   const f16x2 low = {(_Float16)-1032.f, (_Float16)-1032.f};
   const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
   const f16x2 high = {(_Float16)-72.f, (_Float16)-72.f};
-  out[0] = __builtin_bit_cast(f16x2, (w & 0x000F000Fu) | 0x64006400u) + low;
-  out[1] = __builtin_bit_cast(f16x2, (u & 0x000F000Fu) | 0x64006400u) + low;
-  out[2] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (w & 0x00F000F0u) | 0x64006400u), sixteenth, high);
-  out[3] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (u & 0x00F000F0u) | 0x64006400u), sixteenth, high);
+  auto half2 = [](uint32_t v) { return __builtin_bit_cast(f16x2, v); };
+  out[0] = __builtin_bit_cast(uint32_t, half2((w & k.low) | k.exponent) + low);
+  out[1] = __builtin_bit_cast(uint32_t, half2((u & k.low) | k.exponent) + low);
+  out[2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(half2((w & k.high) | k.exponent), sixteenth, high));
+  out[3] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(half2((u & k.high) | k.exponent), sixteenth, high));
 }
 
-__device__ __forceinline__ f16x8 join(f16x2 a, f16x2 b, f16x2 c, f16x2 d) {
-  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+__device__ __forceinline__ f16x8 join(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(f16x8, u32x4{a, b, c, d});
 }
 
-// The lane's share of one 16-token tile.
+__device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Bytes of one step (two tiles), and the LDS-DMA loads that fetch a tile: whole waves of 16 bytes
+// a lane, then the rest.
 template <int NB>
-struct TileRegs {
-  uint32_t k[NB], v[NB];          // quants: one dword per block
-  uint32_t ks[2 * NB], vs[2 * NB];  // fp16 scales [block][4 tokens]
+struct Step {
+  static constexpr int kTile = 576 * NB, kBytes = 2 * kTile;
+  static constexpr int kFull = kTile / 1024, kRest = kTile % 1024 / 16;
+  static constexpr int kLoads = 2 * (kFull + (kRest ? 1 : 0));
 };
 
+// One tile into LDS at `to` (the same for the wave), in kLoads / 2 loads.
 template <int NB>
-__device__ __forceinline__ void load_quants(const uint8_t *p, int lane, uint32_t *out) {
-  typedef __attribute__((address_space(1))) const u32x2a4 *g2;
-  typedef __attribute__((address_space(1))) const u32x3a4 *g3;
+__device__ __forceinline__ void fetch_tile(const uint8_t *p, int lane, uint32_t to) {
+  typedef Step<NB> S;
+  p += lane * 16;
+#pragma unroll
+  for (int i = 0; i < S::kFull; ++i) load_lds16(p + 1024 * i, to + 1024 * i);
+  if (S::kRest && lane < S::kRest) load_lds16(p + 1024 * S::kFull, to + 1024 * S::kFull);
+}
+
+// Waits until at most `ahead` steps' loads are outstanding.
+template <int NB, int MOST>
+__device__ __forceinline__ void wait_steps(int ahead) {
+  if constexpr (MOST == 0) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  } else {
+    if (ahead >= MOST) asm volatile("s_waitcnt vmcnt(%0)" : : "i"(MOST * Step<NB>::kLoads) : "memory");
+    else wait_steps<NB, MOST - 1>(ahead);
+  }
+}
+
+template <int NB>
+__device__ __forceinline__ void read_quants(const uint8_t *p, int lane, uint32_t *out) {
   if constexpr (NB == 2) {
-    const u32x2a4 w = *(g2)(p + lane * 8);
+    const u32x2 w = *(const u32x2 *)(p + lane * 8);
     out[0] = w[0];
     out[1] = w[1];
   } else if constexpr (NB == 3) {
-    const u32x3a4 w = *(g3)(p + lane * 12);
+    const u32x3a4 w = *(const u32x3a4 *)(p + lane * 12);
+#pragma unroll
     for (int i = 0; i < 3; ++i) out[i] = w[i];
   } else {
 #pragma unroll
     for (int c = 0; c < NB / 4; ++c) {
-      const u32x4 w = gload(p + c * 1024 + lane * 16);
+      const u32x4 w = *(const u32x4 *)(p + c * 1024 + lane * 16);
 #pragma unroll
       for (int i = 0; i < 4; ++i) out[4 * c + i] = w[i];
     }
@@ -170,33 +245,23 @@ __device__ __forceinline__ void load_quants(const uint8_t *p, int lane, uint32_t
 }
 
 template <int NB>
-__device__ __forceinline__ void load_scales(const uint8_t *p, int g, uint32_t *out) {
-  typedef __attribute__((address_space(1))) const u32x2 *g2;
+__device__ __forceinline__ void read_scales(const uint8_t *p, int g, uint32_t *out) {
   p += g * 8 * NB;
   if constexpr (NB % 2 == 0) {
 #pragma unroll
     for (int c = 0; c < NB / 2; ++c) {
-      const u32x4 w = gload(p + 16 * c);
+      const u32x4 w = *(const u32x4 *)(p + 16 * c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) out[4 * c + i] = w[i];
     }
   } else {
 #pragma unroll
     for (int c = 0; c < NB; ++c) {
-      const u32x2 w = *(g2)(p + 8 * c);
+      const u32x2 w = *(const u32x2 *)(p + 8 * c);
       out[2 * c] = w[0];
       out[2 * c + 1] = w[1];
     }
   }
-}
-
-template <int NB>
-__device__ __forceinline__ void load_tile(const uint8_t *p, int lane, TileRegs<NB> &t) {
-  constexpr int kQuant = 256 * NB, kHalf = 288 * NB;
-  load_quants<NB>(p, lane, t.k);
-  load_scales<NB>(p + kQuant, lane >> 4, t.ks);
-  load_quants<NB>(p + kHalf, lane, t.v);
-  load_scales<NB>(p + kHalf + kQuant, lane >> 4, t.vs);
 }
 
 // The scale of token 4 g + r of block b as fp32 (folds into mixed-precision FMAs).
@@ -245,66 +310,119 @@ struct Attn {
   static constexpr int D = 32 * NB;
   static constexpr int kPart = NCOL * (D + 2);  // floats of a partial result: m, l, O
   static constexpr int kMergeBlocks = NB < 4 ? NB : 4;  // blocks merged over the waves at a time
+  static constexpr int kAhead = NB == 2 ? 2 : NB == 4 ? KV_AHEAD4 : 1;        // steps that a wave has on their way
+  static constexpr int kRing = kWaves * (kAhead + 1) * Step<NB>::kBytes;
+  static constexpr int kMerge = (2 * kWaves * NCOL + kWaves * NCOL * 32 * kMergeBlocks) * 4;
+  static constexpr int kLds = kRing > kMerge ? kRing : kMerge;
 
   struct State {
     f32x4 o[2 * NB];  // rows 4 g + r (query columns), columns l % 16: dimension 32 b + 16 half + l % 16
     float m, l;       // of column l % 16: reference exponent (shared by the lane groups), this lane's sum
+    int top;          // every value scale so far is below 2^(top - 15) (the same for the wave)
   };
 
+  // p times a value's scale as an fp16 operand: one term, or for SPLIT the second term in the rows
+  // of the second terms (`second` 1).
+  static __device__ __forceinline__ _Float16 weight(float p, float d, float second) {
+    float x = fmaf(p, d, 0.f);
+    if constexpr (SPLIT) {
+      // Both terms from one fp32 value: where the compiler rounds the exact product to fp16 for one
+      // of them and its fp32 rounding for the other, near a tie they are an fp16 step apart.
+      asm("" : "+v"(x));
+      const _Float16 h = (_Float16)x;
+      return (_Float16)fmaf(-(float)h, second, x);
+    }
+    return (_Float16)x;
+  }
+
   // One step of 32 tokens. Reference exponent: weights are p = 2^(s - m) with m such that p times
-  // the value's scale stays below 2^15, the fp16 range, whatever the scales are; m only moves when
-  // a lane would pass that (kSlack binades of slack over the 2^8 it is set to), so the exchange
-  // between lane groups and the rescaling of O are rare. `l` sums p in the same reference.
-  template <bool MASK>
-  static __device__ __forceinline__ void step(const TileRegs<NB> (&t)[2], const f16x8 (&qf)[NB],
-                                              float qs, int lo, int hi, int any_lo, int any_hi,
-                                              int t0, int lane, State &st) {
+  // the value's scale stays below 2^15, the fp16 range, whatever the scales are: m >= s + top - 28 - kSlack
+  // for every token, where top (1, 2, 4, 8 or 16 by one mask test on the scales' exponents, exact
+  // above 16) bounds the scales. m is set without the slack and moves only when a token passes it,
+  // so the exchange between lane groups and the rescaling of O are rare. `l` sums p in the same
+  // reference. `mask` (the same for the wave): some token of the step is hidden from some column.
+  static __device__ __forceinline__ void step(const uint8_t *at, const f16x8 (&qf)[NB], float qs,
+                                              bool mask, int lo, int hi, int any_lo, int any_hi,
+                                              int t0, int lane, float second, State &st) {
+    constexpr int kTile = Step<NB>::kTile, kQuant = 256 * NB, kHalf = 288 * NB;
+    const Unpack uk;
     const int g = lane >> 4;
     float s[8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      uint32_t kq[NB], ks[2 * NB];
+      read_quants<NB>(at + i * kTile, lane, kq);
+      read_scales<NB>(at + i * kTile + kQuant, g, ks);
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        f16x2 n[4];
-        unpack(t[i].k[b], n);
-        const f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(join(n[0], n[1], n[2], n[3]), qf[b],
-                                                               f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        uint32_t n[4];
+        unpack(uk, kq[b], n);
+        const f32x4 d = mfma(join(n[0], n[1], n[2], n[3]), qf[b], f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] = fmaf(scale_of(t[i].ks, b, r), d[r], acc[r]);
+        for (int r = 0; r < 4; ++r) acc[r] = fmaf(scale_of(ks, b, r), d[r], acc[r]);
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         float v = acc[r];
         if constexpr (SPLIT) v += row_swap8(v);  // hi and lo columns of one query
-        if constexpr (MASK) {
-          const int tok = t0 + 16 * i + 4 * g + r;
-          v = tok >= lo && tok < hi ? v : -INFINITY;
-        }
         s[4 * i + r] = v;
       }
     }
-    // largest |scale| of the lane's tokens, as fp16 bits (their order is the magnitudes')
-    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-    u16x2 most = {0, 0};
+    uint32_t vs[2][2 * NB];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) read_scales<NB>(at + i * kTile + kHalf + kQuant, g, vs[i]);
+    // the scales' bits together: they have a bit of exponent 16, 8, 4 ... exactly if one has it
+    uint32_t any_scale = 0;
+    bool odd_scales = false;
+    if (!mask) {
 #pragma unroll
-      for (int j = 0; j < 2 * NB; ++j) {
-        uint32_t w = t[i].vs[j] & 0x7FFF7FFFu;
-        if constexpr (MASK) {  // scales of tokens that no column sees may be anything
-          const int tok = t0 + 16 * i + 4 * g + 2 * (j & 1);
-          if (tok < any_lo || tok >= any_hi) w &= 0xFFFF0000u;
-          if (tok + 1 < any_lo || tok + 1 >= any_hi) w &= 0x0000FFFFu;
-        }
-        most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, w));
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j) any_scale |= vs[i][j];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+        s[i] = tok >= lo && tok < hi ? s[i] : -INFINITY;
       }
-    const int expo = (int)(most[0] > most[1] ? most[0] : most[1]) >> 10;  // scale < 2^(expo - 14)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // scales of tokens that no column sees may be anything: 0
+          const int tok = t0 + 16 * i + 4 * g + 2 * j;
+          const uint32_t keep = (tok >= any_lo && tok < any_hi ? 0xFFFFu : 0u) |
+                                (tok + 1 >= any_lo && tok + 1 < any_hi ? 0xFFFF0000u : 0u);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) any_scale |= vs[i][2 * b + j] &= keep;
+        }
+      odd_scales = __any((any_scale & 0x7C00u) == 0x7C00u || (any_scale & 0x7C000000u) == 0x7C000000u);
+    }
     float mx = s[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
-    float want = fmaf(mx, qs, (float)(expo - 22));
-    if (__any(want > st.m + kSlack)) {
+    auto over = [&](int top) {  // exponents of top and more, for top a power of two up to 16
+      const uint32_t bits = 0x7C00u & ~((uint32_t)(top - 1) << 10);
+      return (any_scale & (bits | bits << 16)) != 0;
+    };
+    float want = fmaf(mx, qs, (float)(st.top - 28));
+    if (__any(over(min(st.top, 16)) || want > st.m + kSlack)) {
+      while (st.top < 16 && __any(over(st.top))) st.top *= 2;
+      if (__any(over(16))) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2 * NB; ++j) {
+            most = max(most, vs[i][j] & 0x7C00u);
+            most = max(most, vs[i][j] >> 16 & 0x7C00u);
+          }
+        int e = (int)(most >> 10) + 1;
+        e = max(e, __shfl_xor(e, 16));
+        e = max(e, __shfl_xor(e, 32));
+        st.top = max(st.top, __builtin_amdgcn_readfirstlane(e));
+      }
+      want = fmaf(mx, qs, (float)(st.top - 28));
       want = fmaxf(want, __shfl_xor(want, 16));
       want = fmaxf(want, __shfl_xor(want, 32));
       const float m = fmaxf(st.m, want);
@@ -324,43 +442,49 @@ struct Attn {
       p[i] = __builtin_amdgcn_exp2f(fmaf(s[i], qs, -st.m));
       st.l += p[i];
     }
+    uint32_t vq[2][NB];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) read_quants<NB>(at + i * kTile + kHalf, lane, vq[i]);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       f16x8 w;
+      if (odd_scales) {  // a hidden token's scale may be no number: 0 times it must stay 0
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = scale_of(t[i >> 2].vs, b, i & 3);
-        float x = fmaf(p[i], d, 0.f);
-        if constexpr (MASK) x = s[i] == -INFINITY ? 0.f : x;  // 0 times a scale that is not a number
-        const _Float16 h = (_Float16)x;
-        if constexpr (SPLIT) w[i] = lane & 8 ? (_Float16)(x - (float)h) : h;
-        else w[i] = h;
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t d2 = opaque(vs[i >> 2][2 * b + (i >> 1 & 1)]);
+          const float d = half_bits_to_float(i & 1 ? d2 >> 16 : d2);
+          w[i] = weight(p[i], s[i] == -INFINITY ? 0.f : d, second);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = weight(p[i], scale_of(vs[i >> 2], b, i & 3), second);
       }
-      f16x2 n0[4], n1[4];
-      unpack(t[0].v[b], n0);
-      unpack(t[1].v[b], n1);
-      st.o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, join(n0[0], n0[1], n1[0], n1[1]), st.o[2 * b], 0, 0, 0);
-      st.o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, join(n0[2], n0[3], n1[2], n1[3]), st.o[2 * b + 1], 0, 0, 0);
+      uint32_t n0[4], n1[4];
+      unpack(uk, vq[0][b], n0);
+      unpack(uk, vq[1][b], n1);
+      st.o[2 * b] = mfma(w, join(n0[0], n0[1], n1[0], n1[1]), st.o[2 * b]);
+      st.o[2 * b + 1] = mfma(w, join(n0[2], n0[3], n1[2], n1[3]), st.o[2 * b + 1]);
     }
   }
 
-  static __device__ __forceinline__ void store_out(const AttnArgs &a, const Request &q, const Columns &c,
+  // Column `col` of a tile whose first row of q is `row`, first head head0, with `per` heads a token.
+  static __device__ __forceinline__ void store_out(const AttnArgs &a, int row, int head0, int per,
                                                    int col, int d, float v) {
-    const int tok = col / c.per, head = c.head0 + col - tok * c.per;
-    T *out = (T *)a.out.data + (int64_t)(q.row0 + c.tok0 + tok) * a.out.row_stride + (int64_t)head * a.out.head_stride;
+    const int tok = col / per, head = head0 + col - tok * per;
+    T *out = (T *)a.out.data + (int64_t)(row + tok) * a.out.row_stride + (int64_t)head * a.out.head_stride;
     out[d] = A::from(v);
   }
-  static __device__ __forceinline__ void store_lse(const AttnArgs &a, const Request &q, const Columns &c,
+  static __device__ __forceinline__ void store_lse(const AttnArgs &a, int row, int head0, int per,
                                                    int col, float m, float l) {
     if (!a.lse) return;
-    const int tok = col / c.per, head = c.head0 + col - tok * c.per;
-    a.lse[(int64_t)(q.row0 + c.tok0 + tok) * (a.group * a.g.heads) + head] =
+    const int tok = col / per, head = head0 + col - tok * per;
+    a.lse[(int64_t)(row + tok) * (a.group * a.g.heads) + head] =
         l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
   }
 
-  // The units [v0, v1) of an item's `steps`, by the whole workgroup.
+  // The units [v0, v1) of an item, by the whole workgroup.
   static __device__ void segment(const AttnArgs &a, const TileShape &ts, const Request &q, int kvh,
-                                 int tile, int v0, int v1, float *part, float *lds) {
+                                 int tile, int v0, int v1, float *part, uint8_t *lds) {
     const int lane = threadIdx.x & 63, wave = wave_index(), g = lane >> 4;
     const Columns cs = columns<NCOL>(a, ts, q, kvh, tile);
     // tokens that the tile's columns see: all together, and this lane's column
@@ -371,6 +495,57 @@ struct Attn {
     const int col = min(SPLIT ? lane & 7 : lane & 15, cs.count - 1);
     const int tok = cs.tok0 + col / cs.per, head = cs.head0 + col % cs.per;
     const int pos = q.first_pos + tok, lo = seen_from(a, pos), hi = max(pos + 1, 0);
+    State st;
+#pragma unroll
+    for (int j = 0; j < 2 * NB; ++j) st.o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    st.m = kLowest;
+    st.l = 0.f;
+    st.top = 1;
+    // the tile's own steps: the item's units are spread over them (a tile of early tokens has fewer)
+    const int s0 = any_lo / 32, n = max(0, (any_hi + 31) / 32 - s0);
+    const double share = (double)n / (double)q.units;  // exact where it has to be: 0 at 0, n at units
+    auto step_at = [&](int v) { return s0 + (v == q.units ? n : (int)(v * share)); };
+    const int from = step_at(v0), to = step_at(v1);
+    const int32_t *table = a.block_table + (int64_t)q.r * a.max_blocks;
+    const int last_block = ((q.len + a.g.page_tokens - 1) >> a.g.page_shift) - 1;
+    const uint8_t *head_data = a.g.data + (int64_t)kvh * a.g.head_bytes;
+    // A tile's address; a page outside the cache reads page 0 (its tokens are masked below).
+    // (constant address space: a scalar load, which does not count among the fetches in flight)
+    auto page_of = [&](int t) {
+      typedef __attribute__((address_space(4))) const int32_t *scalar;
+      return ((scalar)(uintptr_t)table)[__builtin_amdgcn_readfirstlane(min(t >> a.g.page_shift, last_block))];
+    };
+    const unsigned pages = (unsigned)a.g.pages;
+    auto tile_at = [&](int t, int page) {
+      const int64_t ok = (unsigned)page < pages ? page : 0;
+      return head_data + ok * a.g.page_bytes + (int64_t)((t & (a.g.page_tokens - 1)) >> 4) * a.g.tile_bytes;
+    };
+    // Steps from + wave, from + wave + kWaves, ...: kAhead steps of the wave are on their way into
+    // its own ring in LDS (no barriers: a wave waits for its own loads only).
+    const int steps = to - from > wave ? (to - from - wave + kWaves - 1) / kWaves : 0;
+    const uint8_t *ring = lds + wave * (kAhead + 1) * Step<NB>::kBytes;
+    const uint32_t ring_at = lds_address(ring);
+    const float second = lane & 8 ? 1.f : 0.f;
+    auto token_of = [&](int i) { return 32 * (from + wave + i * kWaves); };
+    int fp0 = 0, fp1 = 0;  // pages of the next step to fetch
+    if (steps > 0) {
+      fp0 = page_of(token_of(0));
+      fp1 = page_of(token_of(0) + 16);
+    }
+    unsigned bad_pages = 0;  // two bits for each place of the ring
+    auto fetch = [&](int i) {
+      const int t = token_of(i), place = i % (kAhead + 1);
+      const uint32_t at = ring_at + (uint32_t)place * Step<NB>::kBytes;
+      const unsigned bad = ((unsigned)fp0 >= pages) | ((unsigned)fp1 >= pages) << 1;
+      bad_pages = (bad_pages & ~(3u << (2 * place))) | bad << (2 * place);
+      const uint8_t *p0 = tile_at(t, fp0), *p1 = tile_at(t + 16, fp1);
+      const int tn = token_of(i + 1);
+      fp0 = page_of(tn);
+      fp1 = page_of(tn + 16);
+      fetch_tile<NB>(p0, lane, at);
+      fetch_tile<NB>(p1, lane, at + Step<NB>::kTile);
+    };
+    for (int i = 0; i < kAhead && i < steps; ++i) fetch(i);
     // the query: dimensions 32 b + 4 g + 0..3 and 16 more, times a power of two
     const T *qp = (const T *)a.q.data + (int64_t)(q.row0 + tok) * a.q.row_stride + (int64_t)head * a.q.head_stride;
     f16x8 qf[NB];
@@ -398,63 +573,30 @@ struct Attn {
           else qf[b][i] = h;
         }
     }
-    State st;
-#pragma unroll
-    for (int j = 0; j < 2 * NB; ++j) st.o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    st.m = kLowest;
-    st.l = 0.f;
-    // the tile's own steps: the item's units are spread over them (a tile of early tokens has fewer)
-    const int s0 = any_lo / 32, n = max(0, (any_hi + 31) / 32 - s0);
-    const int from = s0 + (int)((int64_t)v0 * n / q.steps), to = s0 + (int)((int64_t)v1 * n / q.steps);
-    const int32_t *table = a.block_table + (int64_t)q.r * a.max_blocks;
-    const int last_block = ((q.len + a.g.page_tokens - 1) >> a.g.page_shift) - 1;
-    const uint8_t *head_data = a.g.data + (int64_t)kvh * a.g.head_bytes;
-    // A tile's address; a page outside the cache reads page 0 (its tokens are masked below).
-    auto page_of = [&](int t) { return table[min(t >> a.g.page_shift, last_block)]; };
-    auto tile_at = [&](int t, int page) {
-      const int64_t ok = page >= 0 && page < a.g.pages ? page : 0;
-      return head_data + ok * a.g.page_bytes + (int64_t)((t & (a.g.page_tokens - 1)) >> 4) * a.g.tile_bytes;
-    };
-    TileRegs<NB> cur[2], next[2];
-    int s = from + wave;
-    int page0 = 0, page1 = 0;
-    if (s < to) {
-      page0 = page_of(32 * s);
-      page1 = page_of(32 * s + 16);
-      load_tile<NB>(tile_at(32 * s, page0), lane, cur[0]);
-      load_tile<NB>(tile_at(32 * s + 16, page1), lane, cur[1]);
+    for (int i = 0; i < steps; ++i) {
+      // the step that takes the place of the last one read, whose reads have all returned
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      const unsigned bad = bad_pages >> (2 * (i % (kAhead + 1))) & 3u;
+      if (i + kAhead < steps) fetch(i + kAhead);
+      wait_steps<NB, kAhead>(steps - 1 - i);
+      const uint8_t *at = ring + (i % (kAhead + 1)) * Step<NB>::kBytes;
+      const int t0 = token_of(i);
+      const bool inner = t0 >= all_lo && t0 + 32 <= all_hi;
+      const int l0 = bad & 1 ? t0 + 16 : 0, h0 = bad & 2 ? t0 + 16 : 0x7FFFFFFF;
+      step(at, qf, qs, !inner || bad, max(lo, l0), min(hi, h0), max(any_lo, l0), min(any_hi, h0), t0, lane,
+           second, st);
     }
-    while (s < to) {
-      const int s1 = s + kWaves;
-      int np0 = 0, np1 = 0;
-      if (s1 < to) {
-        np0 = page_of(32 * s1);
-        np1 = page_of(32 * s1 + 16);
-        load_tile<NB>(tile_at(32 * s1, np0), lane, next[0]);
-        load_tile<NB>(tile_at(32 * s1 + 16, np1), lane, next[1]);
-      }
-      const int t0 = 32 * s;
-      const bool bad0 = page0 < 0 || page0 >= a.g.pages, bad1 = page1 < 0 || page1 >= a.g.pages;
-      if (t0 >= all_lo && t0 + 32 <= all_hi && !bad0 && !bad1) {
-        step<false>(cur, qf, qs, lo, hi, any_lo, any_hi, t0, lane, st);
-      } else {
-        const int l0 = bad0 ? t0 + 16 : 0, h0 = bad1 ? t0 + 16 : 0x7FFFFFFF;
-        step<true>(cur, qf, qs, max(lo, l0), min(hi, h0), max(any_lo, l0), min(any_hi, h0), t0, lane, st);
-      }
-      cur[0] = next[0];
-      cur[1] = next[1];
-      page0 = np0;
-      page1 = np1;
-      s = s1;
-    }
+    int id = threadIdx.x;  // formed anew: addresses below are not to be kept through the loop above
+    asm volatile("" : "+v"(id));
+    const int l16 = id & 15, grp = id >> 4 & 3;
     // join the waves: sums over the lane groups, then O in runs of up to 128 dimensions
     st.l += __shfl_xor(st.l, 16);
     st.l += __shfl_xor(st.l, 32);
-    float *lm = lds, *ll = lds + kWaves * NCOL, *lo_ = lds + 2 * kWaves * NCOL;
+    float *lm = (float *)lds, *ll = lm + kWaves * NCOL, *lo_ = lm + 2 * kWaves * NCOL;
     __syncthreads();
-    if (lane < NCOL) {
-      lm[wave * NCOL + lane] = st.m;
-      ll[wave * NCOL + lane] = st.l;
+    if ((id & 63) < NCOL) {
+      lm[wave * NCOL + l16] = st.m;
+      ll[wave * NCOL + l16] = st.l;
     }
     constexpr int kRun = 32 * kMergeBlocks;
 #pragma unroll
@@ -466,11 +608,11 @@ struct Attn {
         for (int r = 0; r < 4; ++r) {
           float v = st.o[2 * b0 + j][r];
           if constexpr (SPLIT) v += __shfl_xor(v, 32);
-          const int row = 4 * g + r;
-          if (row < NCOL) lo_[(wave * NCOL + row) * kRun + 16 * j + (lane & 15)] = v;
+          const int row = 4 * grp + r;
+          if (row < NCOL) lo_[(wave * NCOL + row) * kRun + 16 * j + l16] = v;
         }
       __syncthreads();
-      for (int i = threadIdx.x; i < NCOL * kRun; i += kThreads) {
+      for (int i = id; i < NCOL * kRun; i += kThreads) {
         const int c = i / kRun, d = i - c * kRun;
         if (c >= cs.count) continue;
         float m = lm[c], l = 0.f, o = 0.f;
@@ -489,12 +631,18 @@ struct Attn {
             part[NCOL + c] = l;
           }
         } else {
-          store_out(a, q, cs, c, 32 * b0 + d, l == 0.f ? 0.f : o / l);
-          if (b0 == 0 && d == 0) store_lse(a, q, cs, c, m, l);
+          store_out(a, q.row0 + cs.tok0, cs.head0, cs.per, c, 32 * b0 + d, l == 0.f ? 0.f : o / l);
+          if (b0 == 0 && d == 0) store_lse(a, q.row0 + cs.tok0, cs.head0, cs.per, c, m, l);
         }
       }
     }
+    __syncthreads();  // the next segment's fetches go where these sums were
   }
+};
+
+// What k_kv_join needs of the item whose first part a workgroup left (parts 0: none).
+struct JoinItem {
+  int parts, row, head0, per, count;
 };
 
 // Workgroup w takes the units [w per, (w + 1) per). Items that it holds whole are finished here;
@@ -502,16 +650,17 @@ struct Attn {
 // (part 2 w + 1), it leaves partial results for k_kv_join. Bound by HBM (1.125 bytes per key and
 // value element pair).
 template <typename A, int NB, bool SPLIT>
-__global__ __launch_bounds__(kThreads, NB <= 4 ? 2 : 1) void k_kv_attn(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, NB <= 4 ? KV_OCC : 2) void k_kv_attn(AttnArgs a) {
   typedef Attn<A, NB, SPLIT> X;
-  __shared__ float lds[2 * kWaves * X::NCOL + kWaves * X::NCOL * 32 * X::kMergeBlocks];
+  extern __shared__ __align__(16) uint8_t attn_lds[];
   const TileShape ts = tile_shape<X::NCOL>(a.group);
-  const int w = blockIdx.x;
+  // neighbouring shares on one XCD: query tiles of one request read the same keys through one L2
+  const int w = a.grid % 8 ? (int)blockIdx.x : (int)(blockIdx.x % 8 * (a.grid / 8) + blockIdx.x / 8);
   const Place pl = locate(a, ts, [&](int64_t per) { return w * per; });
-  if (pl.r < 0) return;
+  JoinItem join = {0, 0, 0, 0, 0};
   int64_t u = w * pl.per;
-  const int64_t end = min(pl.total, u + pl.per);
-  Request q = request(a, ts, pl.r);
+  const int64_t end = pl.r < 0 ? u : min(pl.total, u + pl.per);
+  Request q = request(a, ts, max(pl.r, 0));
   int64_t base = pl.base;
   while (u < end) {
     int64_t in = u - base;
@@ -520,54 +669,91 @@ __global__ __launch_bounds__(kThreads, NB <= 4 ? 2 : 1) void k_kv_attn(AttnArgs 
       q = request(a, ts, q.r + 1);
       in = u - base;
     }
-    const int64_t item = in / q.steps;
-    const int kvh = (int)(item / q.tiles), tile = (int)(item - (int64_t)kvh * q.tiles);
-    const int v0 = (int)(in - item * q.steps), v1 = (int)min((int64_t)q.steps, v0 + (end - u));
+    const int64_t item = quotient(in, q.units);
+    const int kvh = (int)quotient(item, q.tiles), tile = (int)(item - (int64_t)kvh * q.tiles);
+    const int v0 = (int)(in - item * q.units), v1 = (int)min((int64_t)q.units, v0 + (end - u));
     float *part = nullptr;
-    if (v0 > 0 || v1 < q.steps) part = a.parts + (int64_t)(2 * w + (v0 == 0)) * X::kPart;
-    X::segment(a, ts, q, kvh, tile, v0, v1, part, lds);
+    if (v0 > 0 || v1 < q.units) part = a.parts + (int64_t)(2 * w + (v0 == 0)) * X::kPart;
+    if (v0 == 0 && v1 < q.units) {
+      const Columns cs = columns<X::NCOL>(a, ts, q, kvh, tile);
+      const int64_t last = base + (item + 1) * q.units - 1;
+      join = {(int)(last / pl.per) - w + 1, q.row0 + cs.tok0, cs.head0, cs.per, cs.count};
+    }
+    X::segment(a, ts, q, kvh, tile, v0, v1, part, attn_lds);
     u += v1 - v0;
   }
+  if (threadIdx.x == 0) ((JoinItem *)a.joins)[w] = join;
 }
 
-// Workgroup w joins the parts of the item whose first part workgroup w of k_kv_attn left, if it
-// left one: part 2 w + 1 and the parts 2 w' of the following workgroups up to the item's end.
+// Workgroup (w, y) joins some columns of the item whose first part workgroup w of k_kv_attn left:
+// part 2 w + 1 and the parts 2 w' of the following workgroups. The parts' weights are formed once,
+// side by side; then every output element is a sum over the parts with its loads independent of
+// each other.
+constexpr int kJoinSplit = 4;  // workgroups per item
+
 template <typename A, int NB, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void k_kv_join(AttnArgs a) {
   typedef Attn<A, NB, SPLIT> X;
-  const TileShape ts = tile_shape<X::NCOL>(a.group);
-  const int w = blockIdx.x;
-  const Place pl = locate(a, ts, [&](int64_t per) { return (w + 1) * per - 1; });
-  if (pl.r < 0) return;
-  const Request q = request(a, ts, pl.r);
-  const int64_t e = (w + 1) * pl.per, in = e - 1 - pl.base, item = in / q.steps;
-  const int64_t start = pl.base + item * q.steps, stop = start + q.steps;
-  if (start < w * pl.per || stop <= e) return;
-  const int kvh = (int)(item / q.tiles), tile = (int)(item - (int64_t)kvh * q.tiles);
-  const Columns cs = columns<X::NCOL>(a, ts, q, kvh, tile);
-  const int last = (int)((stop - 1) / pl.per);  // workgroup with the item's last units
-  const float *first = a.parts + (int64_t)(2 * w + 1) * X::kPart;
-  auto part = [&](int i) { return i == w ? first : a.parts + (int64_t)(2 * i) * X::kPart; };
-  for (int i = threadIdx.x; i < cs.count * X::D; i += kThreads) {
-    const int c = i / X::D, d = i - c * X::D;
-    float m = kLowest, l = 0.f, o = 0.f;
-    for (int p = w; p <= last; ++p) {
-      const float *x = part(p);
-      const float pm = x[c], n = fmaxf(m, pm);
-      const float f = __builtin_amdgcn_exp2f(m - n), h = __builtin_amdgcn_exp2f(pm - n);
-      l = fmaf(l, f, h * x[X::NCOL + c]);
-      o = fmaf(o, f, h * x[2 * X::NCOL + c * X::D + d]);
-      m = n;
+  constexpr int kCols = X::NCOL / kJoinSplit;
+  __shared__ float weight[kGrid][kCols];
+  __shared__ float red[2][kWaves][kCols];
+  const int w = blockIdx.x, c0 = blockIdx.y * kCols;
+  const JoinItem item = ((const JoinItem *)a.joins)[w];
+  const int n = item.parts, cols = min(kCols, item.count - c0);
+  if (n == 0 || cols <= 0) return;
+  auto part = [&](int i) { return a.parts + (int64_t)(2 * (w + i) + (i == 0)) * X::kPart; };
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
+  // the largest reference exponent and the sum, of each column
+  float m[kCols], l[kCols];
+  for (int c = 0; c < kCols; ++c) m[c] = kLowest;
+  for (int i = tid; i < n; i += kThreads)
+    for (int c = 0; c < kCols; ++c) m[c] = fmaxf(m[c], part(i)[c0 + c]);
+  for (int c = 0; c < kCols; ++c) {
+    for (int d = 1; d < 64; d <<= 1) m[c] = fmaxf(m[c], __shfl_xor(m[c], d));
+    if (lane == 0) red[0][wave][c] = m[c];
+  }
+  __syncthreads();
+  for (int c = 0; c < kCols; ++c) {
+    for (int v = 0; v < kWaves; ++v) m[c] = fmaxf(m[c], red[0][v][c]);
+    l[c] = 0.f;
+  }
+  for (int i = tid; i < n; i += kThreads)
+    for (int c = 0; c < kCols; ++c) {
+      const float f = __builtin_amdgcn_exp2f(part(i)[c0 + c] - m[c]);
+      weight[i][c] = f;
+      l[c] = fmaf(f, part(i)[X::NCOL + c0 + c], l[c]);
     }
-    X::store_out(a, q, cs, c, d, l == 0.f ? 0.f : o / l);
-    if (d == 0) X::store_lse(a, q, cs, c, m, l);
+  for (int c = 0; c < kCols; ++c) {
+    for (int d = 1; d < 64; d <<= 1) l[c] += __shfl_xor(l[c], d);
+    if (lane == 0) red[1][wave][c] = l[c];
+  }
+  __syncthreads();
+  for (int i = tid; i < cols * X::D; i += kThreads) {
+    const int c = i / X::D, d = i - c * X::D;
+    float o = 0.f, sum = 0.f, top = kLowest;
+    const int at = 2 * X::NCOL + (c0 + c) * X::D + d;
+#pragma unroll 8
+    for (int p = 0; p < n; ++p) o = fmaf(weight[p][c], part(p)[at], o);
+    for (int v = 0; v < kWaves; ++v) {
+      sum += red[1][v][c];
+      top = fmaxf(top, red[0][v][c]);
+    }
+    X::store_out(a, item.row, item.head0, item.per, c0 + c, d, sum == 0.f ? 0.f : o / sum);
+    if (d == 0) X::store_lse(a, item.row, item.head0, item.per, c0 + c, top, sum);
   }
 }
 
 template <typename A, int NB, bool SPLIT>
-int launch(const AttnArgs &a, hipStream_t s) {
-  k_kv_attn<A, NB, SPLIT><<<dim3(a.grid), kThreads, 0, s>>>(a);
-  if (a.grid > 1) k_kv_join<A, NB, SPLIT><<<dim3(a.grid - 1), kThreads, 0, s>>>(a);
+int launch(const AttnArgs &args, hipStream_t s) {
+  AttnArgs a = args;
+  a.joins = a.parts + (int64_t)a.grid * 2 * Attn<A, NB, SPLIT>::kPart;
+  constexpr int kLds = Attn<A, NB, SPLIT>::kLds;
+  if (kLds > 64 * 1024 &&
+      hipFuncSetAttribute(reinterpret_cast<const void *>(&k_kv_attn<A, NB, SPLIT>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kLds) != hipSuccess)
+    return -1;
+  k_kv_attn<A, NB, SPLIT><<<dim3(a.grid), kThreads, kLds, s>>>(a);
+  if (a.grid > 1) k_kv_join<A, NB, SPLIT><<<dim3(a.grid - 1, kJoinSplit), kThreads, 0, s>>>(a);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
@@ -587,7 +773,7 @@ bool split_type(int type) { return type != TQ_BF16; }
 
 size_t kv_attention_workspace(int type, int64_t head_dim, int grid) {
   const int ncol = split_type(type) ? 8 : 16;
-  return (size_t)grid * 2 * ncol * (head_dim + 2) * 4;
+  return (size_t)grid * (2 * ncol * (head_dim + 2) * 4 + sizeof(JoinItem));
 }
 
 int kv_attention_grid(int type, int64_t kv_heads, int64_t head_dim, int64_t group, int64_t rows,
@@ -597,9 +783,9 @@ int kv_attention_grid(int type, int64_t kv_heads, int64_t head_dim, int64_t grou
   const int64_t ncol = split_type(type) ? 8 : 16;
   (void)requests;
   const int64_t tiles = rows * (group <= ncol ? 1 : (group + ncol - 1) / ncol);
-  const int64_t steps = max_len / 32 + 2;
+  const int64_t steps = max_len / 32 + 2 + kItemUnits;
   const double units = (double)tiles * (double)kv_heads * (double)steps;
-  const double most = units / kMinSteps + 1;
+  const double most = units / kMinUnits + 1;
   return most < kGrid ? (int)most : kGrid;
 }
 

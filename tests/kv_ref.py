@@ -163,10 +163,12 @@ def attention(q, k_of, v_of, seq_len, cu_new, kv_heads, scale, window, hidden=No
     magnitudes (32 tokens a product, steps one after another, waves and parts joined).
 
     Weights times a value's scale enter the second product as fp16 numbers x = p d, exact to 2^-25
-    below fp16's normal range, and a nibble is at most 8: out is off by 8 * 2^-25 / l a token, with
-    l = sum p. The kernel takes p = 2^(s - m) with m <= max s + e - 22 for 2^(e - 15) <= max d < 2^(e - 14), so
-    l = max p / max w >= 2^(22 - e) / max w >= 2^7 / (max d * max w), w the softmax weights, and the
-    n tokens add up to n * max w * 2^-29 * max d at most; max d <= max |v| of the row's tokens."""
+    (or lost whole) below fp16's normal range, and a nibble is at most 8: out is off by
+    8 min(2^-25, x) / l a token, with l = sum p. The kernel takes p = 2^(s - m), m <= max s + T - 28,
+    so l = max p / max w >= 2^(28 - T) / max w, w the softmax weights. T bounds the scales,
+    max d < 2^(T - 15); it is a power of two up to 16 with max d >= 2^(T/2 - 15) (subnormal d: T = 1,
+    max d >= 2^-24), or above 16 exact, max d >= 2^(T - 16). So 8 * 2^-25 / l <= 2^(T - 50) max w is at
+    most 2^-27 max w max d (at T = 16; 2^-25 at T = 1), and max d <= max |v| of the row's tokens."""
     q = np.asarray(q, np.float64)
     rows, heads, dim = q.shape
     G = heads // kv_heads
@@ -201,6 +203,7 @@ def attention(q, k_of, v_of, seq_len, cu_new, kv_heads, scale, window, hidden=No
                 dl = 2.0**-18 * s + 2.0**-22 * (np.abs(x).max() + 40)
                 many = (see.sum() / 16 + 64) * 2.0**-23
                 tol[row, h] = mag[row, h] * (2 * np.expm1(dl) + 2 * many)
-                tol[row, h] += see.sum() / tot * 2.0**-29 * np.abs(vv).max()  # max w = 1 / tot
+                far = np.abs(vv).max()  # max w = 1 / tot; x / l = w d, d <= far
+                tol[row, h] += np.minimum((2.0**-27 if far >= 2.0**-14 else 2.0**-25) * far / tot, 8 * far * p / tot).sum()
                 ltol[row, h] = dl + many + 2.0**-22 * (abs(lse[row, h]) + 40)
     return out, lse, tol, ltol, mag
