@@ -457,8 +457,8 @@ class ExpertCache:
 ACT_TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
-def _kv_tensor(t, name: str, dtype, shape, device, strided: bool = False):
-    """Checks a tensor argument of a tq_kv_* call: dtype, shape (None: any), device, density."""
+def _kv_refuse(t, name: str, dtype, shape, device, strided: bool):
+    """Says what is wrong with a tensor argument that _kv_tensor found wrong."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
@@ -467,42 +467,46 @@ def _kv_tensor(t, name: str, dtype, shape, device, strided: bool = False):
         raise ValueError(f"{name} must have the shape {list(shape)}, not {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-    if strided:
-        if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"the last dimension of {name} must be dense")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"the last dimension of {name} must be dense" if strided
+                     else f"{name} must be contiguous")
+
+
+def _kv_tensor(t, name: str, dtype, shape, device, strided: bool = False):
+    """Checks a tensor argument of a tq_kv_* call: dtype, shape (None in it: any size), device,
+    density (strided: of the last dimension only). These calls take microseconds on the device, so
+    the checks are one expression."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+            and (t.shape == shape or (None in shape and len(shape) == t.dim()
+                                      and all(w is None or w == n for w, n in zip(shape, t.shape))))
+            and (t.is_contiguous() or (strided and (t.stride(-1) == 1 or t.shape[-1] <= 1 or not t.numel())))):
+        return t
+    _kv_refuse(t, name, dtype, shape, device, strided)
+
+
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 class _On:
-    """The cache's device and the call's stream as the current ones, where they are not already:
-    outputs and workspaces that a call makes then belong to the stream that uses them. `.handle`
-    is the stream."""
-
-    __slots__ = ("ctx", "handle")
+    """The cache's device and the call's stream as the current ones: outputs and workspaces that a
+    call makes then belong to the stream that uses them."""
 
     def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"the cache is on {device}, not on a GPU")
         if stream is not None and stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the cache on {device}")
-        self.ctx = None
-        if stream is not None:
-            self.ctx = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self.ctx = torch.cuda.device(device)
+        self.ctx = torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        self.handle = torch.cuda.current_stream().cuda_stream
-        return self
+        return self.ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        return False
+        return self.ctx.__exit__(*exc)
+
+
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to change the current device or stream first (_On)."""
+    if device.type != "cuda":
+        raise ValueError(f"the cache is on {device}, not on a GPU")
+    return stream is not None or _current_device() != device.index
 
 
 class KvCache:
@@ -529,6 +533,7 @@ class KvCache:
         d.pages, d.data = self.pages, data.data_ptr()
         self.desc = d
         self.ref = C.byref(d)
+        self.attn_bytes: dict = {}  # workspace sizes of kv_attention by what they depend on
 
 
 class Rope:
@@ -548,8 +553,7 @@ class Rope:
 
 
 def _head_rows(t: torch.Tensor) -> HeadRows:
-    rs, hs, _ = t.stride()
-    return HeadRows(t.data_ptr(), t.shape[1], rs, hs)
+    return HeadRows(t.data_ptr(), t.shape[1], t.stride(0), t.stride(1))
 
 
 def kv_plan(cache: KvCache, kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor,
@@ -573,21 +577,26 @@ def kv_plan(cache: KvCache, kv_len: torch.Tensor, new_len: torch.Tensor, block_t
         _kv_tensor(free_count, "free_count", i32, (1,), dev)
     if rows < 0:
         raise ValueError("rows must not be negative")
-    with _On(dev, stream) as on:
-        out = torch.empty(2 * R + 3 + 3 * rows, dtype=i32, device=dev)
-        cu, seq, count, status, slots, pos, req = out.split([R + 1, R, 1, 1, rows, rows, rows])
-        base = out.data_ptr()
-        at = base + 4 * (2 * R + 3)
-        d = KvStepDesc(R, block_table.shape[1], rows, kv_len.data_ptr(), new_len.data_ptr(),
-                       block_table.data_ptr(), _ptr(free_pages), _ptr(free_count), base,
-                       base + 4 * (R + 1), at if rows else None, at + 4 * rows if rows else None,
-                       at + 8 * rows if rows else None,
-                       base + 4 * (2 * R + 1) if free_pages is not None else None,
-                       base + 4 * (2 * R + 2))
-        _check(lib().tq_kv_plan(cache.ref, C.byref(d), on.handle))
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return kv_plan(cache, kv_len, new_len, block_table, rows, free_pages, free_count)
+    out = torch.empty(2 * R + 3 + 3 * rows, dtype=i32, device=dev)
+    cu, seq, count, status, slots, pos, req = out.split((R + 1, R, 1, 1, rows, rows, rows))
+    base = out.data_ptr()
+    at = base + 4 * (2 * R + 3)
+    managed = free_pages is not None
+    d = KvStepDesc(R, block_table.shape[1], rows, kv_len.data_ptr(), new_len.data_ptr(),
+                   block_table.data_ptr(), free_pages.data_ptr() if managed else None,
+                   free_count.data_ptr() if managed else None, base, base + 4 * (R + 1),
+                   at if rows else None, at + 4 * rows if rows else None,
+                   at + 8 * rows if rows else None, base + 4 * (2 * R + 1) if managed else None,
+                   base + 4 * (2 * R + 2))
+    rc = lib().tq_kv_plan(cache.ref, C.byref(d), _raw_stream(dev.index))
+    if rc:
+        _check(rc)
     res = {"block_table": block_table, "cu_new": cu, "seq_len": seq, "slots": slots,
            "positions": pos, "requests": req, "status": status}
-    if free_pages is not None:
+    if managed:
         res["free_pages"], res["free_count"] = free_pages, count
     return res
 
@@ -623,19 +632,23 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
         _kv_tensor(positions, "positions", torch.int32, (axes, rows), dev, strided=True)
         r = RopeDesc.from_buffer_copy(rope.desc)
         r.positions, r.axis_stride = positions.data_ptr(), positions.stride(0) if axes > 1 else 0
-    with _On(dev, stream) as on:
-        qr = orr = None
-        if q is not None:
-            _kv_tensor(q, "q", k.dtype, (rows, None, D), dev, strided=True)
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            else:
-                _kv_tensor(q_out, "q_out", k.dtype, tuple(q.shape), dev, strided=True)
-            qr, orr = C.byref(_head_rows(q)), C.byref(_head_rows(q_out))
-        if rows:
-            _check(lib().tq_kv_append(cache.ref, ACT_TYPES[k.dtype], rows, slots.data_ptr(),
-                                      C.byref(_head_rows(k)), C.byref(_head_rows(v)), qr, orr,
-                                      None if r is None else C.byref(r), on.handle))
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return kv_append(cache, k, v, slots, q, rope, positions, q_out)
+    qr = orr = None
+    if q is not None:
+        _kv_tensor(q, "q", k.dtype, (rows, None, D), dev, strided=True)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        else:
+            _kv_tensor(q_out, "q_out", k.dtype, q.shape, dev, strided=True)
+        qr, orr = C.byref(_head_rows(q)), C.byref(_head_rows(q_out))
+    if rows:
+        rc = lib().tq_kv_append(cache.ref, ACT_TYPES[k.dtype], rows, slots.data_ptr(),
+                                C.byref(_head_rows(k)), C.byref(_head_rows(v)), qr, orr,
+                                None if r is None else C.byref(r), _raw_stream(dev.index))
+        if rc:
+            _check(rc)
     return q_out
 
 
@@ -647,12 +660,16 @@ def kv_read(cache: KvCache, slots: torch.Tensor, dtype: torch.dtype = torch.floa
     if dtype not in ACT_TYPES:
         raise ValueError("dtype must be fp32, bf16 or fp16")
     rows = slots.shape[0]
-    with _On(dev, stream) as on:
-        k = torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev)
-        v = torch.empty_like(k)
-        if rows:
-            _check(lib().tq_kv_read(cache.ref, ACT_TYPES[dtype], rows, slots.data_ptr(),
-                                    k.data_ptr(), v.data_ptr(), on.handle))
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return kv_read(cache, slots, dtype)
+    k = torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev)
+    v = torch.empty_like(k)
+    if rows:
+        rc = lib().tq_kv_read(cache.ref, ACT_TYPES[dtype], rows, slots.data_ptr(), k.data_ptr(),
+                              v.data_ptr(), _raw_stream(dev.index))
+        if rc:
+            _check(rc)
     return k, v
 
 
@@ -677,21 +694,30 @@ def kv_attention(cache: KvCache, q: torch.Tensor, block_table: torch.Tensor, seq
     _kv_tensor(block_table, "block_table", i32, (R, None), dev)
     _kv_tensor(cu_new, "cu_new", i32, (R + 1,), dev)
     t = ACT_TYPES[q.dtype]
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty((rows, heads, D), dtype=q.dtype, device=dev)
-        else:
-            _kv_tensor(out, "out", q.dtype, (rows, heads, D), dev, strided=True)
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
-        d = KvAttnDesc(rows, R, block_table.shape[1], _head_rows(q), _head_rows(out), _ptr(lse),
-                       block_table.data_ptr(), seq_len.data_ptr(), cu_new.data_ptr(),
-                       D ** -0.5 if scale is None else scale, window)
-        ref = C.byref(d)
-        if ws is None:  # of the calling stream: calls on other streams, and graphs, have their own
-            ws = torch.empty(int(lib().tq_kv_attention_workspace_bytes(cache.ref, t, ref)),
-                             dtype=torch.uint8, device=dev)
-        _check(lib().tq_kv_attention(cache.ref, t, ref, ws.data_ptr() or None,
-                                     ws.numel() * ws.element_size(), on.handle))
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return kv_attention(cache, q, block_table, seq_len, cu_new, scale, window, out,
+                                return_lse, ws)
+    if out is None:
+        out = torch.empty((rows, heads, D), dtype=q.dtype, device=dev)
+    else:
+        _kv_tensor(out, "out", q.dtype, (rows, heads, D), dev, strided=True)
+    lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
+    mb = block_table.shape[1]
+    d = KvAttnDesc(rows, R, mb, _head_rows(q), _head_rows(out), _ptr(lse), block_table.data_ptr(),
+                   seq_len.data_ptr(), cu_new.data_ptr(), D ** -0.5 if scale is None else scale,
+                   window)
+    ref = C.byref(d)
+    if ws is None:  # of the calling stream: calls on other streams, and graphs, have their own
+        need = cache.attn_bytes.get((t, rows, heads, mb))
+        if need is None:
+            need = int(lib().tq_kv_attention_workspace_bytes(cache.ref, t, ref))
+            cache.attn_bytes[t, rows, heads, mb] = need
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    rc = lib().tq_kv_attention(cache.ref, t, ref, ws.data_ptr() or None,
+                               ws.numel() * ws.element_size(), _raw_stream(dev.index))
+    if rc:
+        _check(rc)
     return (out, lse) if return_lse else out
 
 

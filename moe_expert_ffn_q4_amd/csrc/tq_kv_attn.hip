@@ -9,6 +9,8 @@
 // layout of the A operand of the second product: weights stay in the lane that formed them, are
 // multiplied by the values' scale of each block and rounded to fp16 (hi + lo as two rows of the
 // operand for fp32 and fp16 activations).
+#include <atomic>
+
 #include "tq_kv.h"
 #include "tq_kv_device.h"
 #include "tq_launch.h"
@@ -25,18 +27,12 @@ typedef uint32_t u32x3a4 __attribute__((ext_vector_type(3), aligned(4)));
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-#ifndef KV_GRID
-#define KV_GRID 768
-#endif
-#ifndef KV_AHEAD4
-#define KV_AHEAD4 1
-#endif
-#ifndef KV_OCC
-#define KV_OCC 3
-#endif
-constexpr int kGrid = KV_GRID;      // workgroups of a full launch: four per compute unit
+// Workgroups per compute unit, from registers (168 or 256 a lane) and LDS (37 or 74 KB at head_dim
+// 128 and 256); a full launch has just as many, all of them resident at once.
+constexpr int resident(int nb) { return nb <= 4 ? 3 : 2; }
+constexpr int kComputeUnits = 256;
 #ifndef KV_ITEM
-#define KV_ITEM 8
+#define KV_ITEM 16
 #endif
 #ifndef KV_MIN
 #define KV_MIN 8
@@ -308,9 +304,9 @@ struct Attn {
   typedef typename A::type T;
   static constexpr int NCOL = SPLIT ? 8 : 16;  // query columns of a tile
   static constexpr int D = 32 * NB;
-  static constexpr int kPart = NCOL * (D + 2);  // floats of a partial result: m, l, O
+  static constexpr int kPart = NCOL * (D + 2);  // floats of a partial result: m, l, O (16-byte aligned)
   static constexpr int kMergeBlocks = NB < 4 ? NB : 4;  // blocks merged over the waves at a time
-  static constexpr int kAhead = NB == 2 ? 2 : NB == 4 ? KV_AHEAD4 : 1;        // steps that a wave has on their way
+  static constexpr int kAhead = NB == 2 ? 2 : 1;        // steps that a wave has on their way
   static constexpr int kRing = kWaves * (kAhead + 1) * Step<NB>::kBytes;
   static constexpr int kMerge = (2 * kWaves * NCOL + kWaves * NCOL * 32 * kMergeBlocks) * 4;
   static constexpr int kLds = kRing > kMerge ? kRing : kMerge;
@@ -368,6 +364,7 @@ struct Attn {
         if constexpr (SPLIT) v += row_swap8(v);  // hi and lo columns of one query
         s[4 * i + r] = v;
       }
+      if constexpr (NB == 8) __builtin_amdgcn_sched_barrier(0);  // the tiles one by one: registers
     }
     uint32_t vs[2][2 * NB];
 #pragma unroll
@@ -484,7 +481,8 @@ struct Attn {
 
   // The units [v0, v1) of an item, by the whole workgroup.
   static __device__ void segment(const AttnArgs &a, const TileShape &ts, const Request &q, int kvh,
-                                 int tile, int v0, int v1, float *part, uint8_t *lds) {
+                                 int tile, int v0, int v1, int done, int share_units, float *part,
+                                 uint8_t *lds) {
     const int lane = threadIdx.x & 63, wave = wave_index(), g = lane >> 4;
     const Columns cs = columns<NCOL>(a, ts, q, kvh, tile);
     // tokens that the tile's columns see: all together, and this lane's column
@@ -503,6 +501,19 @@ struct Attn {
     st.top = 1;
     // the tile's own steps: the item's units are spread over them (a tile of early tokens has fewer)
     const int s0 = any_lo / 32, n = max(0, (any_hi + 31) / 32 - s0);
+    // A wave that is ahead steps back: priority 3 in the first quarter of the workgroup's share, then
+    // 2, 1, 0. (Issue goes to the oldest wave first: without it the first workgroups of a compute
+    // unit ended after 31 us where the last took 50 us, alone on their SIMDs at the end.)
+    int level = 0, next_level = 0;
+    auto step_back = [&](int i) {
+      if (i < next_level) return;
+      if (level == 0) __builtin_amdgcn_s_setprio(3);
+      else if (level == 1) __builtin_amdgcn_s_setprio(2);
+      else if (level == 2) __builtin_amdgcn_s_setprio(1);
+      else __builtin_amdgcn_s_setprio(0);
+      ++level;
+      next_level = level == 4 ? 0x7FFFFFFF : (level * share_units / 4 - done) / kWaves;
+    };
     const double share = (double)n / (double)q.units;  // exact where it has to be: 0 at 0, n at units
     auto step_at = [&](int v) { return s0 + (v == q.units ? n : (int)(v * share)); };
     const int from = step_at(v0), to = step_at(v1);
@@ -577,6 +588,7 @@ struct Attn {
       // the step that takes the place of the last one read, whose reads have all returned
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       const unsigned bad = bad_pages >> (2 * (i % (kAhead + 1))) & 3u;
+      step_back(i);
       if (i + kAhead < steps) fetch(i + kAhead);
       wait_steps<NB, kAhead>(steps - 1 - i);
       const uint8_t *at = ring + (i % (kAhead + 1)) * Step<NB>::kBytes;
@@ -650,7 +662,7 @@ struct JoinItem {
 // (part 2 w + 1), it leaves partial results for k_kv_join. Bound by HBM (1.125 bytes per key and
 // value element pair).
 template <typename A, int NB, bool SPLIT>
-__global__ __launch_bounds__(kThreads, NB <= 4 ? KV_OCC : 2) void k_kv_attn(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, resident(NB)) void k_kv_attn(AttnArgs a) {
   typedef Attn<A, NB, SPLIT> X;
   extern __shared__ __align__(16) uint8_t attn_lds[];
   const TileShape ts = tile_shape<X::NCOL>(a.group);
@@ -679,68 +691,71 @@ __global__ __launch_bounds__(kThreads, NB <= 4 ? KV_OCC : 2) void k_kv_attn(Attn
       const int64_t last = base + (item + 1) * q.units - 1;
       join = {(int)(last / pl.per) - w + 1, q.row0 + cs.tok0, cs.head0, cs.per, cs.count};
     }
-    X::segment(a, ts, q, kvh, tile, v0, v1, part, attn_lds);
+    X::segment(a, ts, q, kvh, tile, v0, v1, (int)min(u - w * pl.per, (int64_t)1 << 28), (int)min(pl.per, (int64_t)1 << 28), part, attn_lds);
     u += v1 - v0;
   }
   if (threadIdx.x == 0) ((JoinItem *)a.joins)[w] = join;
 }
 
-// Workgroup (w, y) joins some columns of the item whose first part workgroup w of k_kv_attn left:
-// part 2 w + 1 and the parts 2 w' of the following workgroups. The parts' weights are formed once,
-// side by side; then every output element is a sum over the parts with its loads independent of
-// each other.
-constexpr int kJoinSplit = 4;  // workgroups per item
+// Workgroup (w, y) joins the item whose first part workgroup w of k_kv_attn left: part 2 w + 1 and
+// the parts 2 w' of the following workgroups. A thread takes four dimensions of a column and every
+// fourth part. Bound by latency: the parts' references, sums and outputs are read eight parts at a
+// time, at once.
+constexpr int kJoinUnits = 128, kJoinGroups = 4;
 
 template <typename A, int NB, bool SPLIT>
-__global__ __launch_bounds__(kThreads) void k_kv_join(AttnArgs a) {
+__global__ __launch_bounds__(kJoinUnits * kJoinGroups) void k_kv_join(AttnArgs a) {
   typedef Attn<A, NB, SPLIT> X;
-  constexpr int kCols = X::NCOL / kJoinSplit;
-  __shared__ float weight[kGrid][kCols];
-  __shared__ float red[2][kWaves][kCols];
-  const int w = blockIdx.x, c0 = blockIdx.y * kCols;
+  constexpr int kRuns = X::D / 4, kBatch = 8;
+  __shared__ f32x4 other_o[kJoinGroups - 1][kJoinUnits];
+  __shared__ float other_m[kJoinGroups - 1][kJoinUnits], other_l[kJoinGroups - 1][kJoinUnits];
+  const int w = blockIdx.x, unit = threadIdx.x % kJoinUnits, group = threadIdx.x / kJoinUnits;
+  const int i = blockIdx.y * kJoinUnits + unit;
   const JoinItem item = ((const JoinItem *)a.joins)[w];
-  const int n = item.parts, cols = min(kCols, item.count - c0);
-  if (n == 0 || cols <= 0) return;
-  auto part = [&](int i) { return a.parts + (int64_t)(2 * (w + i) + (i == 0)) * X::kPart; };
-  const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
-  // the largest reference exponent and the sum, of each column
-  float m[kCols], l[kCols];
-  for (int c = 0; c < kCols; ++c) m[c] = kLowest;
-  for (int i = tid; i < n; i += kThreads)
-    for (int c = 0; c < kCols; ++c) m[c] = fmaxf(m[c], part(i)[c0 + c]);
-  for (int c = 0; c < kCols; ++c) {
-    for (int d = 1; d < 64; d <<= 1) m[c] = fmaxf(m[c], __shfl_xor(m[c], d));
-    if (lane == 0) red[0][wave][c] = m[c];
+  if (item.parts == 0 || (int)blockIdx.y * kJoinUnits >= item.count * kRuns) return;
+  const int c = i / kRuns, d = (i - c * kRuns) * 4;
+  const bool live = c < item.count;
+  float m = kLowest, l = 0.f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  auto join = [&](float pm, float pl, f32x4 po) {
+    const float top = fmaxf(m, pm);
+    const float f = __builtin_amdgcn_exp2f(m - top), h = __builtin_amdgcn_exp2f(pm - top);
+    l = fmaf(l, f, h * pl);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = fmaf(o[j], f, h * po[j]);
+    m = top;
+  };
+  for (int at = group; live && at < item.parts; at += kBatch * kJoinGroups) {
+    float pm[kBatch], pl[kBatch];
+    f32x4 po[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int n = at + k * kJoinGroups;
+      if (n >= item.parts) break;
+      const float *p = a.parts + (int64_t)(2 * (w + n) + (n == 0)) * X::kPart;
+      pm[k] = p[c];
+      pl[k] = p[X::NCOL + c];
+      po[k] = *(const f32x4 *)(p + 2 * X::NCOL + c * X::D + d);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (at + k * kJoinGroups >= item.parts) break;
+      join(pm[k], pl[k], po[k]);
+    }
+  }
+  if (group > 0) {
+    other_m[group - 1][unit] = m;
+    other_l[group - 1][unit] = l;
+    other_o[group - 1][unit] = o;
   }
   __syncthreads();
-  for (int c = 0; c < kCols; ++c) {
-    for (int v = 0; v < kWaves; ++v) m[c] = fmaxf(m[c], red[0][v][c]);
-    l[c] = 0.f;
-  }
-  for (int i = tid; i < n; i += kThreads)
-    for (int c = 0; c < kCols; ++c) {
-      const float f = __builtin_amdgcn_exp2f(part(i)[c0 + c] - m[c]);
-      weight[i][c] = f;
-      l[c] = fmaf(f, part(i)[X::NCOL + c0 + c], l[c]);
-    }
-  for (int c = 0; c < kCols; ++c) {
-    for (int d = 1; d < 64; d <<= 1) l[c] += __shfl_xor(l[c], d);
-    if (lane == 0) red[1][wave][c] = l[c];
-  }
-  __syncthreads();
-  for (int i = tid; i < cols * X::D; i += kThreads) {
-    const int c = i / X::D, d = i - c * X::D;
-    float o = 0.f, sum = 0.f, top = kLowest;
-    const int at = 2 * X::NCOL + (c0 + c) * X::D + d;
-#pragma unroll 8
-    for (int p = 0; p < n; ++p) o = fmaf(weight[p][c], part(p)[at], o);
-    for (int v = 0; v < kWaves; ++v) {
-      sum += red[1][v][c];
-      top = fmaxf(top, red[0][v][c]);
-    }
-    X::store_out(a, item.row, item.head0, item.per, c0 + c, d, sum == 0.f ? 0.f : o / sum);
-    if (d == 0) X::store_lse(a, item.row, item.head0, item.per, c0 + c, top, sum);
-  }
+  if (group > 0 || !live) return;
+#pragma unroll
+  for (int k = 0; k < kJoinGroups - 1; ++k) join(other_m[k][unit], other_l[k][unit], other_o[k][unit]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    X::store_out(a, item.row, item.head0, item.per, c, d + j, l == 0.f ? 0.f : o[j] / l);
+  if (d == 0) X::store_lse(a, item.row, item.head0, item.per, c, m, l);
 }
 
 template <typename A, int NB, bool SPLIT>
@@ -748,12 +763,22 @@ int launch(const AttnArgs &args, hipStream_t s) {
   AttnArgs a = args;
   a.joins = a.parts + (int64_t)a.grid * 2 * Attn<A, NB, SPLIT>::kPart;
   constexpr int kLds = Attn<A, NB, SPLIT>::kLds;
-  if (kLds > 64 * 1024 &&
-      hipFuncSetAttribute(reinterpret_cast<const void *>(&k_kv_attn<A, NB, SPLIT>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kLds) != hipSuccess)
-    return -1;
+  if (kLds > 64 * 1024) {  // once a device
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return -1;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+      if (hipFuncSetAttribute(reinterpret_cast<const void *>(&k_kv_attn<A, NB, SPLIT>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, kLds) != hipSuccess)
+        return -1;
+      raised.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
   k_kv_attn<A, NB, SPLIT><<<dim3(a.grid), kThreads, kLds, s>>>(a);
-  if (a.grid > 1) k_kv_join<A, NB, SPLIT><<<dim3(a.grid - 1, kJoinSplit), kThreads, 0, s>>>(a);
+  constexpr int kUnits = Attn<A, NB, SPLIT>::NCOL * 8 * NB;  // units of an item
+  if (a.grid > 1)
+    k_kv_join<A, NB, SPLIT><<<dim3(a.grid - 1, (kUnits + kJoinUnits - 1) / kJoinUnits), kJoinUnits * kJoinGroups, 0, s>>>(a);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
@@ -778,7 +803,6 @@ size_t kv_attention_workspace(int type, int64_t head_dim, int grid) {
 
 int kv_attention_grid(int type, int64_t kv_heads, int64_t head_dim, int64_t group, int64_t rows,
                       int64_t requests, int64_t max_len) {
-  (void)head_dim;
   // an upper bound of the units: every row a tile of its own over the longest sequence
   const int64_t ncol = split_type(type) ? 8 : 16;
   (void)requests;
@@ -786,7 +810,8 @@ int kv_attention_grid(int type, int64_t kv_heads, int64_t head_dim, int64_t grou
   const int64_t steps = max_len / 32 + 2 + kItemUnits;
   const double units = (double)tiles * (double)kv_heads * (double)steps;
   const double most = units / kMinUnits + 1;
-  return most < kGrid ? (int)most : kGrid;
+  const int full = kComputeUnits * resident((int)(head_dim / 32));
+  return most < full ? (int)most : full;
 }
 
 int launch_kv_attention(int type, const AttnArgs &a, hipStream_t s) {
