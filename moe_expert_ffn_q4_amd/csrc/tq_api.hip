@@ -981,7 +981,7 @@ int kv_attn_check(const tq_kv_cache *c, int type, const tq_kv_attn *t, bool poin
   a.block_table = t->block_table;
   a.seq_len = t->seq_len;
   a.cu_new = t->cu_new;
-  a.grid = tq::kv_attention_grid(type, c->kv_heads, c->head_dim, a.group, t->rows, t->requests, t->max_blocks * c->page_tokens);
+  a.grid = tq::kv_attention_grid(type, c->kv_heads, c->head_dim, a.group, t->rows, t->max_blocks * c->page_tokens);
   *out = a;
   return TQ_OK;
 }
@@ -1124,7 +1124,7 @@ int tq_kv_read(const tq_kv_cache *c, int type, int64_t rows, const int32_t *slot
 size_t tq_kv_attention_workspace_bytes(const tq_kv_cache *c, int type, const tq_kv_attn *t) {
   tq::AttnArgs a;
   if (kv_attn_check(c, type, t, false, &a) != TQ_OK) return 0;
-  return tq::kv_attention_workspace(type, c->head_dim, a.grid);
+  return tq::kv_attention_workspace(type, c->head_dim, a.group, a.rows, a.requests, a.grid);
 }
 
 int tq_kv_attention(const tq_kv_cache *c, int type, const tq_kv_attn *t, void *workspace, size_t ws_bytes, void *stream) {
@@ -1132,7 +1132,7 @@ int tq_kv_attention(const tq_kv_cache *c, int type, const tq_kv_attn *t, void *w
   const int rc = kv_attn_check(c, type, t, true, &a);
   if (rc != TQ_OK) return rc;
   if (a.rows == 0) return TQ_OK;
-  const size_t need = tq::kv_attention_workspace(type, c->head_dim, a.grid);
+  const size_t need = tq::kv_attention_workspace(type, c->head_dim, a.group, a.rows, a.requests, a.grid);
   if (!workspace) return fail(TQ_EINVAL, "tq_kv_attention: null workspace");
   if (!aligned(workspace, 256)) return fail(TQ_EALIGN, "tq_kv_attention: workspace must be 256-byte aligned");
   if (ws_bytes < need) return fail(TQ_ENOSPC, "tq_kv_attention: workspace of %zu bytes, %zu needed", ws_bytes, need);

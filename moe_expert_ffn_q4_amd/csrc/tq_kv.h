@@ -84,6 +84,7 @@ struct ReadArgs {
 struct AttnArgs {
   KvGeom g;
   int rows, requests, max_blocks, group, grid;
+  int wide_cols;  // set by the launch
   int window;     // tokens a row sees, itself included; 0: all
   float scale;    // softmax scale times log2(e)
   HeadRows q, out;
@@ -98,10 +99,9 @@ struct AttnArgs {
 int launch_kv_plan(const PlanArgs &a, hipStream_t s);
 int launch_kv_append(int type, const AppendArgs &a, hipStream_t s);
 int launch_kv_read(int type, const ReadArgs &a, hipStream_t s);
-size_t kv_attention_workspace(int type, int64_t head_dim, int grid);
+size_t kv_attention_workspace(int type, int64_t head_dim, int64_t group, int64_t rows, int64_t requests, int grid);
 // Workgroups of the attention launch (each takes an equal share of the step's key tiles).
-int kv_attention_grid(int type, int64_t kv_heads, int64_t head_dim, int64_t group, int64_t rows,
-                      int64_t requests, int64_t max_len);
+int kv_attention_grid(int type, int64_t kv_heads, int64_t head_dim, int64_t group, int64_t rows, int64_t max_len);
 int launch_kv_attention(int type, const AttnArgs &a, hipStream_t s);
 
 }  // namespace tq

@@ -42,6 +42,15 @@ constexpr int kItemUnits = KV_ITEM;    // what an item costs beside its steps (q
 constexpr float kLowest = -3.4028234663852886e38f;
 constexpr float kSlack = 2.f;    // see step()
 
+// A request with more query columns a kv head (new tokens x heads) than this goes to k_kv_wide, if
+// that is launched: from an average of as many a request. TODO
+constexpr int kWideCols = 32;
+constexpr int kWideGrid = 2 * kComputeUnits;
+
+bool split_type(int type) { return type != TQ_BF16; }
+
+bool wide_launch(int64_t group, int64_t rows, int64_t requests) { return rows * group > kWideCols * requests; }
+
 // ---- the step's work as one line of units -----------------------------------------------------
 // An item is a query tile (up to NCOL columns: tokens x heads of one kv head) of a request; its
 // units are the 32-token steps of its request and kItemUnits for what it costs beside them. All
@@ -69,6 +78,9 @@ __device__ __forceinline__ int seen_from(const AttnArgs &a, int pos) {
   return a.window ? max(0, pos - a.window + 1) : 0;
 }
 
+// WIDE: of the requests with more than wide_cols query columns a kv head, else of the others; a
+// request of the other class has no tiles.
+template <bool WIDE>
 __device__ __forceinline__ Request request(const AttnArgs &a, const TileShape &ts, int r) {
   Request q;
   q.r = r;
@@ -76,7 +88,8 @@ __device__ __forceinline__ Request request(const AttnArgs &a, const TileShape &t
   q.fresh = max(min(a.cu_new[r + 1], a.rows) - q.row0, 0);
   q.len = (int)min((int64_t)max(a.seq_len[r], 0), (int64_t)a.max_blocks << a.g.page_shift);
   q.first_pos = q.len - q.fresh;
-  q.tiles = (q.fresh + ts.tokens - 1) / ts.tokens * ts.splits;
+  const bool wide = (int64_t)q.fresh * a.group > a.wide_cols;
+  q.tiles = wide == WIDE ? (q.fresh + ts.tokens - 1) / ts.tokens * ts.splits : 0;
   q.units = kItemUnits + max(0, (q.len + 31) / 32 - seen_from(a, q.first_pos) / 32);
   return q;
 }
@@ -110,7 +123,7 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
 }
 
 // Called by every thread of the workgroup. `unit_of(per)`: the wanted unit.
-template <typename F>
+template <bool WIDE, typename F>
 __device__ __forceinline__ Place locate(const AttnArgs &a, const TileShape &ts, F unit_of) {
   __shared__ int64_t sums[kWaves];
   __shared__ int64_t found[2];
@@ -118,7 +131,7 @@ __device__ __forceinline__ Place locate(const AttnArgs &a, const TileShape &ts, 
   const int n = (a.requests + kThreads - 1) / kThreads;
   const int r0 = min(a.requests, tid * n), r1 = min(a.requests, r0 + n);
   int64_t mine = 0;
-  for (int r = r0; r < r1; ++r) mine += units_of(a, request(a, ts, r));
+  for (int r = r0; r < r1; ++r) mine += units_of(a, request<WIDE>(a, ts, r));
   int64_t incl = mine;
   for (int d = 1; d < 64; d <<= 1) {
     const int64_t y = __shfl_up(incl, d);
@@ -139,7 +152,7 @@ __device__ __forceinline__ Place locate(const AttnArgs &a, const TileShape &ts, 
   const int64_t u = unit_of(p.per);
   if (u >= base && u < base + mine) {
     for (int r = r0; r < r1; ++r) {
-      const int64_t m = units_of(a, request(a, ts, r));
+      const int64_t m = units_of(a, request<WIDE>(a, ts, r));
       if (u < base + m) {
         found[0] = r;
         found[1] = base;
@@ -297,7 +310,152 @@ __device__ __forceinline__ Columns columns(const AttnArgs &a, const TileShape &t
   return c;
 }
 
-// ---- the kernel ---------------------------------------------------------------------------------
+// ---- softmax over steps -----------------------------------------------------------------------
+
+// Running results of CT query tiles of 16 columns.
+template <int NB, int CT>
+struct State {
+  f32x4 o[CT][2 * NB];  // rows 4 g + r (columns of the tile), columns l % 16: dimension 32 b + 16 half + l % 16
+  float m[CT], l[CT];   // of column l % 16: reference exponent (shared by the lane groups), this lane's sum
+  int top;              // every value scale so far is below 2^(top - 15) (the same for the wave)
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+#pragma unroll
+      for (int j = 0; j < 2 * NB; ++j) o[c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      m[c] = kLowest;
+      l[c] = 0.f;
+    }
+    top = 1;
+  }
+};
+
+// The bits of a step's value scales together: they have a bit of exponent 16, 8, 4 ... exactly if
+// one of them has it. With `mask`, scales of tokens outside any_lo .. any_hi (which no column sees and
+// which may be anything) become 0, and `odd` says whether one may be no number.
+template <int NB>
+__device__ __forceinline__ uint32_t scale_bits(uint32_t (&vs)[2][2 * NB], bool mask, int any_lo, int any_hi,
+                                               int t0, int g, bool &odd) {
+  uint32_t bits = 0;
+  odd = false;
+  if (!mask) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2 * NB; ++j) bits |= vs[i][j];
+    return bits;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int tok = t0 + 16 * i + 4 * g + 2 * j;
+      const uint32_t keep = (tok >= any_lo && tok < any_hi ? 0xFFFFu : 0u) |
+                            (tok + 1 >= any_lo && tok + 1 < any_hi ? 0xFFFF0000u : 0u);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) bits |= vs[i][2 * b + j] &= keep;
+    }
+  odd = __any((bits & 0x7C00u) == 0x7C00u || (bits & 0x7C000000u) == 0x7C000000u);
+  return bits;
+}
+
+// Logits s (of the lane's 8 tokens, times qs) to weights p = 2^(s - m), in place, with the sums and
+// outputs so far brought to the same reference m: such that p times the value's scale stays below
+// 2^15, the fp16 range, whatever the scales are. m >= s + top - 28 - kSlack for every token, where
+// top (1, 2, 4, 8 or 16 by one mask test on the scales' exponents, exact above 16) bounds the scales.
+// m is set without the slack and moves only when a token passes it, so the exchange between lane
+// groups and the rescaling of O are rare.
+template <int NB, int CT>
+__device__ __forceinline__ void weigh(float (&s)[CT][8], const float (&qs)[CT], const uint32_t (&vs)[2][2 * NB],
+                                      uint32_t bits, int g, State<NB, CT> &st) {
+  auto over = [&](int top) {  // exponents of top and more, for top a power of two up to 16
+    const uint32_t b = 0x7C00u & ~((uint32_t)(top - 1) << 10);
+    return (bits & (b | b << 16)) != 0;
+  };
+  float mx[CT];
+  bool move = over(min(st.top, 16));
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    mx[c] = s[c][0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) mx[c] = fmaxf(mx[c], s[c][i]);
+    move |= fmaf(mx[c], qs[c], (float)(st.top - 28)) > st.m[c] + kSlack;
+  }
+  if (__any(move)) {
+    while (st.top < 16 && __any(over(st.top))) st.top *= 2;
+    if (__any(over(16))) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j) {
+          most = max(most, vs[i][j] & 0x7C00u);
+          most = max(most, vs[i][j] >> 16 & 0x7C00u);
+        }
+      int e = (int)(most >> 10) + 1;
+      e = max(e, __shfl_xor(e, 16));
+      e = max(e, __shfl_xor(e, 32));
+      st.top = max(st.top, __builtin_amdgcn_readfirstlane(e));
+    }
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      float want = fmaf(mx[c], qs[c], (float)(st.top - 28));
+      want = fmaxf(want, __shfl_xor(want, 16));
+      want = fmaxf(want, __shfl_xor(want, 32));
+      const float m = fmaxf(st.m[c], want);
+      const float alpha = __builtin_amdgcn_exp2f(st.m[c] - m);
+      st.m[c] = m;
+      st.l[c] *= alpha;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float f = __shfl(alpha, 4 * g + r);
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j) st.o[c][j][r] *= f;
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s[c][i] = __builtin_amdgcn_exp2f(fmaf(s[c][i], qs[c], -st.m[c]));
+      st.l[c] += s[c][i];
+    }
+}
+
+// Scale of token i (of the lane's 8) of block b, taken as 0 where the column (which sees lo .. hi)
+// does not see the token: its bits may be no number, and 0 times it must stay 0. Its own copy of
+// the bits, so that the usual path keeps its half-register operands.
+__device__ __forceinline__ float odd_scale(const uint32_t *vs, int b, int i, int t0, int g, int lo, int hi) {
+  const uint32_t d2 = opaque(vs[2 * b + (i >> 1 & 1)]);
+  const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+  return tok >= lo && tok < hi ? half_bits_to_float(i & 1 ? d2 >> 16 : d2) : 0.f;
+}
+
+// The power of two that a query row with largest magnitude `most` is multiplied by.
+__device__ __forceinline__ int query_exponent(float most) {
+  return most > 0.f && most < INFINITY ? min(15 - __builtin_amdgcn_frexp_expf(most), 100) : 0;
+}
+
+// Column `col` of a tile whose first row of q is `row`, first head head0, with `per` heads a token.
+template <typename A>
+__device__ __forceinline__ void store_out(const AttnArgs &a, int row, int head0, int per, int col, int d,
+                                          float v) {
+  const int tok = col / per, head = head0 + col - tok * per;
+  typename A::type *out = (typename A::type *)a.out.data + (int64_t)(row + tok) * a.out.row_stride +
+                          (int64_t)head * a.out.head_stride;
+  out[d] = A::from(v);
+}
+__device__ __forceinline__ void store_lse(const AttnArgs &a, int row, int head0, int per, int col, float m,
+                                          float l) {
+  if (!a.lse) return;
+  const int tok = col / per, head = head0 + col - tok * per;
+  a.lse[(int64_t)(row + tok) * (a.group * a.g.heads) + head] =
+      l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+}
+
+// ---- few columns: waves share an item's steps ----------------------------------------------------
 
 template <typename A, int NB, bool SPLIT>
 struct Attn {
@@ -311,11 +469,8 @@ struct Attn {
   static constexpr int kMerge = (2 * kWaves * NCOL + kWaves * NCOL * 32 * kMergeBlocks) * 4;
   static constexpr int kLds = kRing > kMerge ? kRing : kMerge;
 
-  struct State {
-    f32x4 o[2 * NB];  // rows 4 g + r (query columns), columns l % 16: dimension 32 b + 16 half + l % 16
-    float m, l;       // of column l % 16: reference exponent (shared by the lane groups), this lane's sum
-    int top;          // every value scale so far is below 2^(top - 15) (the same for the wave)
-  };
+  static constexpr bool kWide = false;
+  typedef A Act;
 
   // p times a value's scale as an fp16 operand: one term, or for SPLIT the second term in the rows
   // of the second terms (`second` 1).
@@ -331,19 +486,14 @@ struct Attn {
     return (_Float16)x;
   }
 
-  // One step of 32 tokens. Reference exponent: weights are p = 2^(s - m) with m such that p times
-  // the value's scale stays below 2^15, the fp16 range, whatever the scales are: m >= s + top - 28 - kSlack
-  // for every token, where top (1, 2, 4, 8 or 16 by one mask test on the scales' exponents, exact
-  // above 16) bounds the scales. m is set without the slack and moves only when a token passes it,
-  // so the exchange between lane groups and the rescaling of O are rare. `l` sums p in the same
-  // reference. `mask` (the same for the wave): some token of the step is hidden from some column.
+  // One step of 32 tokens; `mask` (the same for the wave): some token is hidden from some column.
   static __device__ __forceinline__ void step(const uint8_t *at, const f16x8 (&qf)[NB], float qs,
                                               bool mask, int lo, int hi, int any_lo, int any_hi,
-                                              int t0, int lane, float second, State &st) {
+                                              int t0, int lane, float second, State<NB, 1> &st) {
     constexpr int kTile = Step<NB>::kTile, kQuant = 256 * NB, kHalf = 288 * NB;
     const Unpack uk;
     const int g = lane >> 4;
-    float s[8];
+    float s[1][8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t kq[NB], ks[2 * NB];
@@ -362,96 +512,34 @@ struct Attn {
       for (int r = 0; r < 4; ++r) {
         float v = acc[r];
         if constexpr (SPLIT) v += row_swap8(v);  // hi and lo columns of one query
-        s[4 * i + r] = v;
+        s[0][4 * i + r] = v;
       }
       if constexpr (NB == 8) __builtin_amdgcn_sched_barrier(0);  // the tiles one by one: registers
     }
     uint32_t vs[2][2 * NB];
 #pragma unroll
     for (int i = 0; i < 2; ++i) read_scales<NB>(at + i * kTile + kHalf + kQuant, g, vs[i]);
-    // the scales' bits together: they have a bit of exponent 16, 8, 4 ... exactly if one has it
-    uint32_t any_scale = 0;
-    bool odd_scales = false;
-    if (!mask) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2 * NB; ++j) any_scale |= vs[i][j];
-    } else {
+    if (mask) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
-        s[i] = tok >= lo && tok < hi ? s[i] : -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {  // scales of tokens that no column sees may be anything: 0
-          const int tok = t0 + 16 * i + 4 * g + 2 * j;
-          const uint32_t keep = (tok >= any_lo && tok < any_hi ? 0xFFFFu : 0u) |
-                                (tok + 1 >= any_lo && tok + 1 < any_hi ? 0xFFFF0000u : 0u);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) any_scale |= vs[i][2 * b + j] &= keep;
-        }
-      odd_scales = __any((any_scale & 0x7C00u) == 0x7C00u || (any_scale & 0x7C000000u) == 0x7C000000u);
-    }
-    float mx = s[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
-    auto over = [&](int top) {  // exponents of top and more, for top a power of two up to 16
-      const uint32_t bits = 0x7C00u & ~((uint32_t)(top - 1) << 10);
-      return (any_scale & (bits | bits << 16)) != 0;
-    };
-    float want = fmaf(mx, qs, (float)(st.top - 28));
-    if (__any(over(min(st.top, 16)) || want > st.m + kSlack)) {
-      while (st.top < 16 && __any(over(st.top))) st.top *= 2;
-      if (__any(over(16))) {
-        uint32_t most = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2 * NB; ++j) {
-            most = max(most, vs[i][j] & 0x7C00u);
-            most = max(most, vs[i][j] >> 16 & 0x7C00u);
-          }
-        int e = (int)(most >> 10) + 1;
-        e = max(e, __shfl_xor(e, 16));
-        e = max(e, __shfl_xor(e, 32));
-        st.top = max(st.top, __builtin_amdgcn_readfirstlane(e));
-      }
-      want = fmaf(mx, qs, (float)(st.top - 28));
-      want = fmaxf(want, __shfl_xor(want, 16));
-      want = fmaxf(want, __shfl_xor(want, 32));
-      const float m = fmaxf(st.m, want);
-      const float alpha = __builtin_amdgcn_exp2f(st.m - m);
-      st.m = m;
-      st.l *= alpha;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float f = __shfl(alpha, 4 * g + r);
-#pragma unroll
-        for (int j = 0; j < 2 * NB; ++j) st.o[j][r] *= f;
+        s[0][i] = tok >= lo && tok < hi ? s[0][i] : -INFINITY;
       }
     }
-    float p[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(fmaf(s[i], qs, -st.m));
-      st.l += p[i];
-    }
+    bool odd;
+    const uint32_t bits = scale_bits<NB>(vs, mask, any_lo, any_hi, t0, g, odd);
+    const float qs1[1] = {qs};
+    weigh<NB, 1>(s, qs1, vs, bits, g, st);
+    const float (&p)[8] = s[0];
     uint32_t vq[2][NB];
 #pragma unroll
     for (int i = 0; i < 2; ++i) read_quants<NB>(at + i * kTile + kHalf, lane, vq[i]);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       f16x8 w;
-      if (odd_scales) {  // a hidden token's scale may be no number: 0 times it must stay 0
+      if (odd) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t d2 = opaque(vs[i >> 2][2 * b + (i >> 1 & 1)]);
-          const float d = half_bits_to_float(i & 1 ? d2 >> 16 : d2);
-          w[i] = weight(p[i], s[i] == -INFINITY ? 0.f : d, second);
-        }
+        for (int i = 0; i < 8; ++i) w[i] = weight(p[i], odd_scale(vs[i >> 2], b, i, t0, g, lo, hi), second);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = weight(p[i], scale_of(vs[i >> 2], b, i & 3), second);
@@ -459,24 +547,9 @@ struct Attn {
       uint32_t n0[4], n1[4];
       unpack(uk, vq[0][b], n0);
       unpack(uk, vq[1][b], n1);
-      st.o[2 * b] = mfma(w, join(n0[0], n0[1], n1[0], n1[1]), st.o[2 * b]);
-      st.o[2 * b + 1] = mfma(w, join(n0[2], n0[3], n1[2], n1[3]), st.o[2 * b + 1]);
+      st.o[0][2 * b] = mfma(w, join(n0[0], n0[1], n1[0], n1[1]), st.o[0][2 * b]);
+      st.o[0][2 * b + 1] = mfma(w, join(n0[2], n0[3], n1[2], n1[3]), st.o[0][2 * b + 1]);
     }
-  }
-
-  // Column `col` of a tile whose first row of q is `row`, first head head0, with `per` heads a token.
-  static __device__ __forceinline__ void store_out(const AttnArgs &a, int row, int head0, int per,
-                                                   int col, int d, float v) {
-    const int tok = col / per, head = head0 + col - tok * per;
-    T *out = (T *)a.out.data + (int64_t)(row + tok) * a.out.row_stride + (int64_t)head * a.out.head_stride;
-    out[d] = A::from(v);
-  }
-  static __device__ __forceinline__ void store_lse(const AttnArgs &a, int row, int head0, int per,
-                                                   int col, float m, float l) {
-    if (!a.lse) return;
-    const int tok = col / per, head = head0 + col - tok * per;
-    a.lse[(int64_t)(row + tok) * (a.group * a.g.heads) + head] =
-        l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
   }
 
   // The units [v0, v1) of an item, by the whole workgroup.
@@ -493,12 +566,8 @@ struct Attn {
     const int col = min(SPLIT ? lane & 7 : lane & 15, cs.count - 1);
     const int tok = cs.tok0 + col / cs.per, head = cs.head0 + col % cs.per;
     const int pos = q.first_pos + tok, lo = seen_from(a, pos), hi = max(pos + 1, 0);
-    State st;
-#pragma unroll
-    for (int j = 0; j < 2 * NB; ++j) st.o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    st.m = kLowest;
-    st.l = 0.f;
-    st.top = 1;
+    State<NB, 1> st;
+    st.clear();
     // the tile's own steps: the item's units are spread over them (a tile of early tokens has fewer)
     const int s0 = any_lo / 32, n = max(0, (any_hi + 31) / 32 - s0);
     // A wave that is ahead steps back: priority 3 in the first quarter of the workgroup's share, then
@@ -572,7 +641,7 @@ struct Attn {
         }
       most = fmaxf(most, __shfl_xor(most, 16));
       most = fmaxf(most, __shfl_xor(most, 32));
-      const int e = most > 0.f && most < INFINITY ? min(15 - __builtin_amdgcn_frexp_expf(most), 100) : 0;
+      const int e = query_exponent(most);
       qs = ldexpf(a.scale, -e);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -602,13 +671,13 @@ struct Attn {
     asm volatile("" : "+v"(id));
     const int l16 = id & 15, grp = id >> 4 & 3;
     // join the waves: sums over the lane groups, then O in runs of up to 128 dimensions
-    st.l += __shfl_xor(st.l, 16);
-    st.l += __shfl_xor(st.l, 32);
+    st.l[0] += __shfl_xor(st.l[0], 16);
+    st.l[0] += __shfl_xor(st.l[0], 32);
     float *lm = (float *)lds, *ll = lm + kWaves * NCOL, *lo_ = lm + 2 * kWaves * NCOL;
     __syncthreads();
     if ((id & 63) < NCOL) {
-      lm[wave * NCOL + l16] = st.m;
-      ll[wave * NCOL + l16] = st.l;
+      lm[wave * NCOL + l16] = st.m[0];
+      ll[wave * NCOL + l16] = st.l[0];
     }
     constexpr int kRun = 32 * kMergeBlocks;
 #pragma unroll
@@ -618,7 +687,7 @@ struct Attn {
       for (int j = 0; j < 2 * kMergeBlocks; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float v = st.o[2 * b0 + j][r];
+          float v = st.o[0][2 * b0 + j][r];
           if constexpr (SPLIT) v += __shfl_xor(v, 32);
           const int row = 4 * grp + r;
           if (row < NCOL) lo_[(wave * NCOL + row) * kRun + 16 * j + l16] = v;
@@ -643,7 +712,7 @@ struct Attn {
             part[NCOL + c] = l;
           }
         } else {
-          store_out(a, q.row0 + cs.tok0, cs.head0, cs.per, c, 32 * b0 + d, l == 0.f ? 0.f : o / l);
+          store_out<A>(a, q.row0 + cs.tok0, cs.head0, cs.per, c, 32 * b0 + d, l == 0.f ? 0.f : o / l);
           if (b0 == 0 && d == 0) store_lse(a, q.row0 + cs.tok0, cs.head0, cs.per, c, m, l);
         }
       }
@@ -652,33 +721,448 @@ struct Attn {
   }
 };
 
+// ---- many columns: waves share an item's keys and values -----------------------------------------
+
+// A workgroup takes 64 CT query columns, 16 CT a wave. Each wave unpacks a quarter of a step (one
+// tile of keys or of values) into LDS in the matrix cores' operand layout, so a nibble is unpacked
+// once for 64 CT columns, and all waves read all of it. Two stages: a step is unpacked while the
+// step before it is multiplied, one barrier a step; raw quants are on their way two steps ahead.
+// Bound by vector issue, so the values' scales are applied where it costs least: for bf16
+// activations to the values, once, as they are unpacked (rounded to fp16, 2^-12 of a value, against
+// 2^-9 in the output; a tile's values are brought to [0, 8) by a power of two, which the softmax
+// weights take up); for fp32 and fp16 to the weights, which then enter as two fp16 terms.
+template <typename A, int NB, bool SPLIT>
+struct Wide {
+  typedef A Act;
+  typedef typename A::type T;
+  static constexpr bool kWide = true;
+  static constexpr int CT = NB == 8 ? 1 : 2;
+  static constexpr int NCOL = kWaves * 16 * CT;
+  static constexpr int D = 32 * NB;
+  static constexpr int kPart = NCOL * (D + 2);
+  static constexpr int kQueryTerms = sizeof(T) == 4 ? 2 : 1;  // fp16 and bf16 queries are one term
+  // offsets in a stage: key operands, value operands, scales, then what Header holds
+  static constexpr int kValues = 2048 * NB, kScales = 4096 * NB, kHeader = 4224 * NB;
+  static constexpr int kStage = kHeader + 32;
+  static constexpr int kLds = 2 * kStage;
+
+  struct Header {  // of a step's two tiles
+    uint32_t no_page[2];  // the tile's page is outside the cache
+    uint32_t odd[2];      // a scale of its values is no number
+    int exponent[2];      // its values are stored times 2^-exponent
+    int unused[2];
+  };
+
+  struct Raw {
+    uint32_t q[NB], s;  // the lane's share of a tile's key or value quants; a dword of its scales
+    uint32_t no_page;
+  };
+
+  static __device__ __forceinline__ void load(const uint8_t *p, int lane, Raw &r) {
+    typedef __attribute__((address_space(1))) const u32x2 *g2;
+    typedef __attribute__((address_space(1))) const u32x3a4 *g3;
+    typedef __attribute__((address_space(1))) const uint32_t *g1;
+    if constexpr (NB == 2) {
+      const u32x2 w = *(g2)(p + lane * 8);
+      r.q[0] = w[0];
+      r.q[1] = w[1];
+    } else if constexpr (NB == 3) {
+      const u32x3a4 w = *(g3)(p + lane * 12);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) r.q[i] = w[i];
+    } else {
+#pragma unroll
+      for (int c = 0; c < NB / 4; ++c) {
+        const u32x4 w = gload(p + c * 1024 + lane * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.q[4 * c + i] = w[i];
+      }
+    }
+    r.s = lane < 8 * NB ? *(g1)(p + 256 * NB + lane * 4) : 0u;
+  }
+
+  // Tile i of the step as operands into a stage.
+  static __device__ __forceinline__ void unpack_into(uint8_t *stage, bool values, int i, int lane, Raw &r) {
+    const Unpack uk;
+    Header *head = (Header *)(stage + kHeader);
+    uint8_t *scales = stage + kScales + ((values ? 2 : 0) + i) * 32 * NB;
+    if (lane < 8 * NB) *(uint32_t *)(scales + lane * 4) = r.s;
+    if (!values) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t n[4];
+        unpack(uk, r.q[b], n);
+        *(u32x4 *)(stage + (i * NB + b) * 1024 + lane * 16) = u32x4{n[0], n[1], n[2], n[3]};
+      }
+      if (lane == 0) head->no_page[i] = r.no_page;
+      return;
+    }
+    f16x2 d[2 * NB];
+    if constexpr (!SPLIT) {
+      uint32_t raw[2 * NB];  // (this wave's own store above)
+      read_scales<NB>(scales, lane >> 4, raw);
+      typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+      auto exponent = [&]() {
+        u16x2 most = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j)
+          most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, raw[j] & 0x7C007C00u));
+        int top = max((int)most[0], (int)most[1]) >> 10;
+        top = max(top, __shfl_xor(top, 16));
+        return __builtin_amdgcn_readfirstlane(max(top, __shfl_xor(top, 32)));
+      };
+      int top = exponent();
+      const bool odd = top == 31;
+      if (odd) {  // not numbers as 0 here, and the columns that see them afterwards: see_odd()
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j) {
+          if ((raw[j] & 0x7C00u) == 0x7C00u) raw[j] &= 0xFFFF0000u;
+          if ((raw[j] & 0x7C000000u) == 0x7C000000u) raw[j] &= 0x0000FFFFu;
+        }
+        top = exponent();
+      }
+      const int e = top - 14;  // scales below 2^e, e -14 .. 16
+      const _Float16 f = (_Float16)ldexpf(1.f, -e);
+#pragma unroll
+      for (int j = 0; j < 2 * NB; ++j) d[j] = __builtin_bit_cast(f16x2, raw[j]) * f16x2{f, f};
+      if (lane == 0) {
+        head->odd[i] = odd;
+        head->exponent[i] = e;
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      uint32_t n[4];
+      unpack(uk, r.q[b], n);
+      if constexpr (!SPLIT) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          n[k] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, n[k]) * d[2 * b + (k & 1)]);
+      }
+      uint8_t *v = stage + kValues + 2 * b * 1024 + lane * 16 + 8 * i;
+      *(u32x2 *)v = u32x2{n[0], n[1]};
+      *(u32x2 *)(v + 1024) = u32x2{n[2], n[3]};
+    }
+  }
+
+  template <typename F>
+  static __device__ __forceinline__ void weights(const float (&p)[8], F scale, f16x8 &w0, f16x8 &w1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = scale(i);
+      float x = fmaf(p[i], d, 0.f);
+      if constexpr (SPLIT) {
+        asm("" : "+v"(x));  // both terms from one fp32 value
+        w0[i] = (_Float16)x;
+        w1[i] = (_Float16)(x - (float)w0[i]);
+      } else {
+        w0[i] = (_Float16)x;
+      }
+    }
+  }
+
+  static __device__ __forceinline__ void step(const uint8_t *stage, const f16x8 (&qf)[CT][kQueryTerms][NB],
+                                              const float (&qs)[CT], bool mask, const int (&lo)[CT],
+                                              const int (&hi)[CT], int any_lo, int any_hi, int t0, int lane,
+                                              State<NB, CT> &st, int (&odd)[CT]) {
+    const int g = lane >> 4;
+    float s[CT][8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t ks[2 * NB];
+      read_scales<NB>(stage + kScales + i * 32 * NB, g, ks);
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[c][4 * i + r] = 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const f16x8 k = *(const f16x8 *)(stage + (i * NB + b) * 1024 + lane * 16);
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int t = kQueryTerms - 1; t >= 0; --t) d = mfma(k, qf[c][t][b], d);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[c][4 * i + r] = fmaf(scale_of(ks, b, r), d[r], s[c][4 * i + r]);
+        }
+      }
+    }
+    if (mask) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+          s[c][i] = tok >= lo[c] && tok < hi[c] ? s[c][i] : -INFINITY;
+        }
+    }
+    if constexpr (SPLIT) scaled_weights(stage, s, qs, mask, lo, hi, any_lo, any_hi, t0, lane, st);
+    else scaled_values(stage, s, qs, mask, lo, hi, t0, lane, st, odd);
+  }
+
+  static __device__ __forceinline__ void scaled_weights(const uint8_t *stage, float (&s)[CT][8], const float (&qs)[CT],
+                                                        bool mask, const int (&lo)[CT], const int (&hi)[CT],
+                                                        int any_lo, int any_hi, int t0, int lane, State<NB, CT> &st) {
+    const int g = lane >> 4;
+    uint32_t vs[2][2 * NB];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) read_scales<NB>(stage + kScales + (2 + i) * 32 * NB, g, vs[i]);
+    bool odd;
+    const uint32_t bits = scale_bits<NB>(vs, mask, any_lo, any_hi, t0, g, odd);
+    weigh<NB, CT>(s, qs, vs, bits, g, st);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const f16x8 v0 = *(const f16x8 *)(stage + kValues + 2 * b * 1024 + lane * 16);
+      const f16x8 v1 = *(const f16x8 *)(stage + kValues + (2 * b + 1) * 1024 + lane * 16);
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        f16x8 w0, w1;
+        if (odd) weights(s[c], [&](int i) { return odd_scale(vs[i >> 2], b, i, t0, g, lo[c], hi[c]); }, w0, w1);
+        else weights(s[c], [&](int i) { return scale_of(vs[i >> 2], b, i & 3); }, w0, w1);
+        st.o[c][2 * b] = mfma(w0, v0, st.o[c][2 * b]);
+        st.o[c][2 * b + 1] = mfma(w0, v1, st.o[c][2 * b + 1]);
+        if constexpr (SPLIT) {
+          st.o[c][2 * b] = mfma(w1, v0, st.o[c][2 * b]);
+          st.o[c][2 * b + 1] = mfma(w1, v1, st.o[c][2 * b + 1]);
+        }
+      }
+    }
+  }
+
+  // Weights p = 2^(s - m + e) for values times 2^-e: m is moved where a weight would pass 2^15 and then
+  // set so that the largest is 2^8 (see weigh()); the sums take p 2^-e.
+  static __device__ __forceinline__ void scaled_values(const uint8_t *stage, float (&s)[CT][8], const float (&qs)[CT],
+                                                       bool mask, const int (&lo)[CT], const int (&hi)[CT], int t0,
+                                                       int lane, State<NB, CT> &st, int (&odd)[CT]) {
+    const int g = lane >> 4;
+    const Header *head = (const Header *)(stage + kHeader);
+    const float e[2] = {(float)head->exponent[0], (float)head->exponent[1]};
+    const float back[2] = {__builtin_amdgcn_exp2f(-e[0]), __builtin_amdgcn_exp2f(-e[1])};
+    bool move = false;
+    float want[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      float mx[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        mx[i] = fmaf(fmaxf(fmaxf(s[c][4 * i], s[c][4 * i + 1]), fmaxf(s[c][4 * i + 2], s[c][4 * i + 3])), qs[c], e[i]);
+      want[c] = fmaxf(mx[0], mx[1]) - 8.f;
+      move |= want[c] > st.m[c] + 7.f;
+    }
+    if (__any(move)) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        float w = fmaxf(want[c], __shfl_xor(want[c], 16));
+        w = fmaxf(w, __shfl_xor(w, 32));
+        const float m = fmaxf(st.m[c], w);
+        const float alpha = __builtin_amdgcn_exp2f(st.m[c] - m);
+        st.m[c] = m;
+        st.l[c] *= alpha;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float f = __shfl(alpha, 4 * g + r);
+#pragma unroll
+          for (int j = 0; j < 2 * NB; ++j) st.o[c][j][r] *= f;
+        }
+      }
+    }
+    f16x8 w[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      const float off[2] = {e[0] - st.m[c], e[1] - st.m[c]};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[c][i], qs[c], off[i >> 2]));
+        st.l[c] = fmaf(p, back[i >> 2], st.l[c]);
+        w[c][i] = (_Float16)p;
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const f16x8 v0 = *(const f16x8 *)(stage + kValues + 2 * b * 1024 + lane * 16);
+      const f16x8 v1 = *(const f16x8 *)(stage + kValues + (2 * b + 1) * 1024 + lane * 16);
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        st.o[c][2 * b] = mfma(w[c], v0, st.o[c][2 * b]);
+        st.o[c][2 * b + 1] = mfma(w[c], v1, st.o[c][2 * b + 1]);
+      }
+    }
+    if (__builtin_amdgcn_readfirstlane(head->odd[0] | head->odd[1])) see_odd(stage, mask, lo, hi, t0, g, odd);
+  }
+
+  // Bit b of odd[c]: the lane's column sees one of the lane's tokens whose block b has a scale that is no
+  // number (its values entered as 0; finish() makes the column's outputs of the block no numbers).
+  static __device__ __forceinline__ void see_odd(const uint8_t *stage, bool mask, const int (&lo)[CT],
+                                                 const int (&hi)[CT], int t0, int g, int (&odd)[CT]) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+      const uint8_t *scales = stage + kScales + (2 + (i >> 2)) * 32 * NB + g * 8 * NB + 2 * (i & 3);
+      int bits = 0;
+      for (int b = 0; b < NB; ++b) bits |= (*(const uint16_t *)(scales + 8 * b) & 0x7C00u) == 0x7C00u ? 1 << b : 0;
+#pragma unroll
+      for (int c = 0; c < CT; ++c) odd[c] |= !mask || (tok >= lo[c] && tok < hi[c]) ? bits : 0;
+    }
+  }
+
+  // The units [v0, v1) of an item, by the whole workgroup.
+  static __device__ void segment(const AttnArgs &a, const TileShape &ts, const Request &q, int kvh, int tile,
+                                 int v0, int v1, int done, int share_units, float *part, uint8_t *lds) {
+    (void)done;
+    (void)share_units;
+    const int lane = threadIdx.x & 63, wave = wave_index(), g = lane >> 4;
+    const Columns cs = columns<NCOL>(a, ts, q, kvh, tile);
+    const int last_tok = cs.tok0 + (cs.count - 1) / cs.per;
+    const int any_lo = seen_from(a, q.first_pos + cs.tok0), any_hi = max(q.first_pos + last_tok + 1, 0);
+    // this wave's columns (none: it unpacks only), and what they see: all together, and each
+    const int c0 = wave * 16 * CT, mine = min(cs.count - c0, 16 * CT);
+    const int tok_a = cs.tok0 + min(c0, cs.count - 1) / cs.per;
+    const int tok_b = cs.tok0 + (min(c0 + 16 * CT, cs.count) - 1) / cs.per;
+    const int mine_lo = seen_from(a, q.first_pos + tok_a), mine_hi = max(q.first_pos + tok_b + 1, 0);
+    const int all_lo = seen_from(a, q.first_pos + tok_b), all_hi = max(q.first_pos + tok_a + 1, 0);
+    const int s0 = any_lo / 32, n = max(0, (any_hi + 31) / 32 - s0);
+    const double share = (double)n / (double)q.units;
+    auto step_at = [&](int v) { return s0 + (v == q.units ? n : (int)(v * share)); };
+    const int from = step_at(v0), steps = step_at(v1) - from;
+    const int32_t *table = a.block_table + (int64_t)q.r * a.max_blocks;
+    const int last_block = ((q.len + a.g.page_tokens - 1) >> a.g.page_shift) - 1;
+    const unsigned pages = (unsigned)a.g.pages;
+    const bool values = wave >= 2;
+    const int half = wave & 1;  // the tile of a step that this wave unpacks
+    const uint8_t *head_data = a.g.data + (int64_t)kvh * a.g.head_bytes + (values ? a.g.half_bytes : 0);
+    auto page_of = [&](int t) {
+      typedef __attribute__((address_space(4))) const int32_t *scalar;
+      return ((scalar)(uintptr_t)table)[__builtin_amdgcn_readfirstlane(min(t >> a.g.page_shift, last_block))];
+    };
+    auto fetch = [&](int i, Raw &r) {  // past the end the last step again
+      const int t = 32 * (from + min(i, steps - 1)) + 16 * half;
+      const int page = page_of(t);
+      const int64_t ok = (unsigned)page < pages ? page : 0;
+      r.no_page = (unsigned)page >= pages;
+      load(head_data + ok * a.g.page_bytes + (int64_t)((t & (a.g.page_tokens - 1)) >> 4) * a.g.tile_bytes, lane, r);
+    };
+    Raw raw0, raw1;
+    if (steps > 0) {
+      fetch(0, raw0);
+      fetch(1, raw1);
+    }
+    f16x8 qf[CT][kQueryTerms][NB];
+    float qs[CT];
+    int lo[CT], hi[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      const int col = min(c0 + 16 * c + (lane & 15), cs.count - 1);
+      const int tok = cs.tok0 + col / cs.per, head = cs.head0 + col % cs.per, pos = q.first_pos + tok;
+      lo[c] = seen_from(a, pos);
+      hi[c] = max(pos + 1, 0);
+      const T *qp = (const T *)a.q.data + (int64_t)(q.row0 + tok) * a.q.row_stride + (int64_t)head * a.q.head_stride;
+      // read twice rather than kept: the values beside everything else would spill
+      auto element = [&](int b, int i) { return A::load(qp + 32 * b + 4 * g + (i & 3) + 16 * (i >> 2)); };
+      float most = 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(element(b, i)));
+      most = fmaxf(most, __shfl_xor(most, 16));
+      most = fmaxf(most, __shfl_xor(most, 32));
+      const int e = query_exponent(most);
+      qs[c] = ldexpf(a.scale, -e);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = ldexpf(element(b, i), e);
+          const _Float16 h = (_Float16)x;
+          qf[c][0][b][i] = h;
+          if constexpr (kQueryTerms == 2) qf[c][1][b][i] = (_Float16)(x - (float)h);
+        }
+      }
+    }
+    State<NB, CT> st;
+    st.clear();
+    int odd[CT] = {};
+    auto turn = [&](int i, Raw &r, uint8_t *stage) {
+      unpack_into(stage, values, half, lane, r);
+      fetch(i + 2, r);
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      const int t0 = 32 * (from + i);
+      if (mine <= 0 || t0 >= mine_hi || t0 + 32 <= mine_lo) return;
+      const Header *head = (const Header *)(stage + kHeader);
+      const bool bad0 = __builtin_amdgcn_readfirstlane(head->no_page[0]), bad1 = __builtin_amdgcn_readfirstlane(head->no_page[1]);
+      const bool inner = t0 >= all_lo && t0 + 32 <= all_hi && !bad0 && !bad1;
+      const int l0 = bad0 ? t0 + 16 : 0, h0 = bad1 ? t0 + 16 : 0x7FFFFFFF;
+      int lo1[CT], hi1[CT];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        lo1[c] = max(lo[c], l0);
+        hi1[c] = min(hi[c], h0);
+      }
+      step(stage, qf, qs, !inner, lo1, hi1, max(mine_lo, l0), min(mine_hi, h0), t0, lane, st, odd);
+    };
+    for (int i = 0; i < steps; i += 2) {
+      turn(i, raw0, lds);
+      if (i + 1 < steps) turn(i + 1, raw1, lds + kStage);
+    }
+    const int l16 = lane & 15;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      float l = st.l[c];
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      int nan_blocks = odd[c] | __shfl_xor(odd[c], 16);
+      nan_blocks |= __shfl_xor(nan_blocks, 32);
+      const int own = c0 + 16 * c + l16;
+      if (g == 0 && own < cs.count) {
+        if (part) {
+          part[own] = st.m[c];
+          part[NCOL + own] = l;
+        } else {
+          store_lse(a, q.row0 + cs.tok0, cs.head0, cs.per, own, st.m[c], l);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float sum = __shfl(l, 4 * g + r), inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int col = c0 + 16 * c + 4 * g + r, nans = __shfl(nan_blocks, 4 * g + r);
+        if (col >= cs.count) continue;
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j) {
+          const float v = nans >> (j >> 1) & 1 ? NAN : st.o[c][j][r];
+          if (part) part[2 * NCOL + col * D + 16 * j + l16] = v;
+          else store_out<A>(a, q.row0 + cs.tok0, cs.head0, cs.per, col, 16 * j + l16, v * inv);
+        }
+      }
+    }
+    __syncthreads();  // the next segment's first steps go where this one's last may still be read
+  }
+};
+
 // What k_kv_join needs of the item whose first part a workgroup left (parts 0: none).
 struct JoinItem {
   int parts, row, head0, per, count;
 };
 
-// Workgroup w takes the units [w per, (w + 1) per). Items that it holds whole are finished here;
-// of the others, at most one begun before its share (part 2 w) and one that ends behind it
-// (part 2 w + 1), it leaves partial results for k_kv_join. Bound by HBM (1.125 bytes per key and
-// value element pair).
-template <typename A, int NB, bool SPLIT>
-__global__ __launch_bounds__(kThreads, resident(NB)) void k_kv_attn(AttnArgs a) {
-  typedef Attn<A, NB, SPLIT> X;
-  extern __shared__ __align__(16) uint8_t attn_lds[];
+// Workgroup w takes the units [w per, (w + 1) per) of the class's items. Items that it holds whole
+// are finished here; of the others, at most one begun before its share (part 2 w) and one that ends
+// behind it (part 2 w + 1), it leaves partial results for k_kv_join.
+template <typename X>
+__device__ __forceinline__ void take_share(AttnArgs &a, uint8_t *lds) {
   const TileShape ts = tile_shape<X::NCOL>(a.group);
   // neighbouring shares on one XCD: query tiles of one request read the same keys through one L2
   const int w = a.grid % 8 ? (int)blockIdx.x : (int)(blockIdx.x % 8 * (a.grid / 8) + blockIdx.x / 8);
-  const Place pl = locate(a, ts, [&](int64_t per) { return w * per; });
+  const Place pl = locate<X::kWide>(a, ts, [&](int64_t per) { return w * per; });
   JoinItem join = {0, 0, 0, 0, 0};
   int64_t u = w * pl.per;
   const int64_t end = pl.r < 0 ? u : min(pl.total, u + pl.per);
-  Request q = request(a, ts, max(pl.r, 0));
+  Request q = request<X::kWide>(a, ts, max(pl.r, 0));
   int64_t base = pl.base;
   while (u < end) {
     int64_t in = u - base;
-    while (in >= units_of(a, q)) {  // on to the next request (one without new tokens has no units)
+    while (in >= units_of(a, q)) {  // on to the next request (some have no units)
       base += units_of(a, q);
-      q = request(a, ts, q.r + 1);
+      q = request<X::kWide>(a, ts, q.r + 1);
       in = u - base;
     }
     const int64_t item = quotient(in, q.units);
@@ -691,10 +1175,26 @@ __global__ __launch_bounds__(kThreads, resident(NB)) void k_kv_attn(AttnArgs a) 
       const int64_t last = base + (item + 1) * q.units - 1;
       join = {(int)(last / pl.per) - w + 1, q.row0 + cs.tok0, cs.head0, cs.per, cs.count};
     }
-    X::segment(a, ts, q, kvh, tile, v0, v1, (int)min(u - w * pl.per, (int64_t)1 << 28), (int)min(pl.per, (int64_t)1 << 28), part, attn_lds);
+    X::segment(a, ts, q, kvh, tile, v0, v1, (int)min(u - w * pl.per, (int64_t)1 << 28),
+               (int)min(pl.per, (int64_t)1 << 28), part, lds);
     u += v1 - v0;
   }
   if (threadIdx.x == 0) ((JoinItem *)a.joins)[w] = join;
+}
+
+// Bound by HBM (1.125 bytes per key and value element pair) and, close to it, by vector issue.
+template <typename A, int NB, bool SPLIT>
+__global__ __launch_bounds__(kThreads, resident(NB)) void k_kv_attn(AttnArgs a) {
+  extern __shared__ __align__(16) uint8_t attn_lds[];
+  take_share<Attn<A, NB, SPLIT>>(a, attn_lds);
+}
+
+// Bound by vector issue: 32 scale products, 8 exponentials and 32 weights a lane for 16 matrix
+// products of 16 columns.
+template <typename A, int NB, bool SPLIT>
+__global__ __launch_bounds__(kThreads, 2) void k_kv_wide(AttnArgs a) {
+  extern __shared__ __align__(16) uint8_t attn_lds[];
+  take_share<Wide<A, NB, SPLIT>>(a, attn_lds);
 }
 
 // Workgroup (w, y) joins the item whose first part workgroup w of k_kv_attn left: part 2 w + 1 and
@@ -703,9 +1203,8 @@ __global__ __launch_bounds__(kThreads, resident(NB)) void k_kv_attn(AttnArgs a) 
 // time, at once.
 constexpr int kJoinUnits = 128, kJoinGroups = 4;
 
-template <typename A, int NB, bool SPLIT>
+template <typename X>
 __global__ __launch_bounds__(kJoinUnits * kJoinGroups) void k_kv_join(AttnArgs a) {
-  typedef Attn<A, NB, SPLIT> X;
   constexpr int kRuns = X::D / 4, kBatch = 8;
   __shared__ f32x4 other_o[kJoinGroups - 1][kJoinUnits];
   __shared__ float other_m[kJoinGroups - 1][kJoinUnits], other_l[kJoinGroups - 1][kJoinUnits];
@@ -754,32 +1253,45 @@ __global__ __launch_bounds__(kJoinUnits * kJoinGroups) void k_kv_join(AttnArgs a
   for (int k = 0; k < kJoinGroups - 1; ++k) join(other_m[k][unit], other_l[k][unit], other_o[k][unit]);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    X::store_out(a, item.row, item.head0, item.per, c, d + j, l == 0.f ? 0.f : o[j] / l);
-  if (d == 0) X::store_lse(a, item.row, item.head0, item.per, c, m, l);
+    store_out<typename X::Act>(a, item.row, item.head0, item.per, c, d + j, l == 0.f ? 0.f : o[j] / l);
+  if (d == 0) store_lse(a, item.row, item.head0, item.per, c, m, l);
 }
 
-template <typename A, int NB, bool SPLIT>
-int launch(const AttnArgs &args, hipStream_t s) {
+// The kernel `K` over X's items with `grid` workgroups, then their join.
+template <typename X, void (*K)(AttnArgs)>
+int launch_class(const AttnArgs &args, int grid, hipStream_t s) {
   AttnArgs a = args;
-  a.joins = a.parts + (int64_t)a.grid * 2 * Attn<A, NB, SPLIT>::kPart;
-  constexpr int kLds = Attn<A, NB, SPLIT>::kLds;
-  if (kLds > 64 * 1024) {  // once a device
+  a.grid = grid;
+  a.joins = a.parts + (int64_t)grid * 2 * X::kPart;
+  if (X::kLds > 64 * 1024) {  // once a device
     static std::atomic<uint64_t> raised{0};
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) return -1;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(raised.load(std::memory_order_relaxed) & bit)) {
-      if (hipFuncSetAttribute(reinterpret_cast<const void *>(&k_kv_attn<A, NB, SPLIT>),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, kLds) != hipSuccess)
+      if (hipFuncSetAttribute(reinterpret_cast<const void *>(K), hipFuncAttributeMaxDynamicSharedMemorySize,
+                              X::kLds) != hipSuccess)
         return -1;
       raised.fetch_or(bit, std::memory_order_relaxed);
     }
   }
-  k_kv_attn<A, NB, SPLIT><<<dim3(a.grid), kThreads, kLds, s>>>(a);
-  constexpr int kUnits = Attn<A, NB, SPLIT>::NCOL * 8 * NB;  // units of an item
-  if (a.grid > 1)
-    k_kv_join<A, NB, SPLIT><<<dim3(a.grid - 1, (kUnits + kJoinUnits - 1) / kJoinUnits), kJoinUnits * kJoinGroups, 0, s>>>(a);
+  K<<<dim3(grid), kThreads, X::kLds, s>>>(a);
+  constexpr int kUnits = X::NCOL * X::D / 4;  // units of an item
+  if (grid > 1)
+    k_kv_join<X><<<dim3(grid - 1, (kUnits + kJoinUnits - 1) / kJoinUnits), kJoinUnits * kJoinGroups, 0, s>>>(a);
   return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+template <typename A, int NB, bool SPLIT>
+int launch(const AttnArgs &args, hipStream_t s) {
+  AttnArgs a = args;
+  const bool wide = wide_launch(a.group, a.rows, a.requests);
+  a.wide_cols = wide ? kWideCols : INT32_MAX;
+  if (wide) {
+    const int rc = launch_class<Wide<A, NB, SPLIT>, k_kv_wide<A, NB, SPLIT>>(a, kWideGrid, s);
+    if (rc) return rc;
+  }
+  return launch_class<Attn<A, NB, SPLIT>, k_kv_attn<A, NB, SPLIT>>(a, a.grid, s);
 }
 
 template <typename A, bool SPLIT>
@@ -792,20 +1304,20 @@ int launch_dim(const AttnArgs &a, hipStream_t s) {
   }
 }
 
-bool split_type(int type) { return type != TQ_BF16; }
-
 }  // namespace
 
-size_t kv_attention_workspace(int type, int64_t head_dim, int grid) {
-  const int ncol = split_type(type) ? 8 : 16;
-  return (size_t)grid * (2 * ncol * (head_dim + 2) * 4 + sizeof(JoinItem));
+size_t kv_attention_workspace(int type, int64_t head_dim, int64_t group, int64_t rows, int64_t requests, int grid) {
+  auto bytes = [&](int64_t workgroups, int64_t columns) {
+    return (size_t)(workgroups * (2 * columns * (head_dim + 2) * 4 + (int64_t)sizeof(JoinItem)));
+  };
+  const size_t few = bytes(grid, split_type(type) ? 8 : 16);
+  const size_t many = wide_launch(group, rows, requests) ? bytes(kWideGrid, head_dim == 256 ? 64 : 128) : 0;
+  return few > many ? few : many;
 }
 
-int kv_attention_grid(int type, int64_t kv_heads, int64_t head_dim, int64_t group, int64_t rows,
-                      int64_t requests, int64_t max_len) {
+int kv_attention_grid(int type, int64_t kv_heads, int64_t head_dim, int64_t group, int64_t rows, int64_t max_len) {
   // an upper bound of the units: every row a tile of its own over the longest sequence
   const int64_t ncol = split_type(type) ? 8 : 16;
-  (void)requests;
   const int64_t tiles = rows * (group <= ncol ? 1 : (group + ncol - 1) / ncol);
   const int64_t steps = max_len / 32 + 2 + kItemUnits;
   const double units = (double)tiles * (double)kv_heads * (double)steps;

@@ -450,6 +450,90 @@ def test_attention_values_that_are_not_numbers():
             check_attention(good, q64[keep], out[keep], lse[keep], [4, 1], t, 64**-0.5, 0)
 
 
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("kv,G,dim,page,lens,news,window", [
+    (1, 4, 128, 16, [200], [200], 0),                    # a prompt from nothing
+    (2, 1, 64, 32, [300, 33, 170], [130, 33, 170], 0),   # one head a group: 130 columns are two tiles
+    (1, 5, 96, 64, [260, 1], [77, 1], 40),               # a window; tiles of 125 of 128 columns
+    (1, 3, 256, 16, [150, 90], [150, 30], 0),
+    (1, 160, 64, 16, [70], [3], 0),                      # more heads than a tile has columns
+    (2, 8, 128, 64, [3000, 60], [40, 60], 0),            # cut over workgroups
+])
+def test_attention_prompts(kv, G, dim, page, lens, news, window, t):
+    """Requests with many new tokens, whose tiles share unpacked keys and values."""
+    _case("attention prompts", kv, G, dim, page, lens, news, window, t)
+    attention_case(dim + window, t, kv, G, dim, page, lens, news, window)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scale,spread,qscale", [(6000.0, 1.3, 1e-4), (1e-5, 8.0, 1e4), (0.1, 300.0, 0.3),
+                                                 (0.3, 1.0, 12.0), (0.3, 1.0, 0.0)])
+def test_attention_prompt_ranges(scale, spread, qscale, t):
+    _case("attention prompt ranges", scale, spread, qscale, t)
+    attention_case(17, t, 2, 4, 64, 16, [250, 90], [50, 33], qscale=qscale, scale=scale, spread=spread)
+
+
+def test_attention_prompt_values_that_are_not_numbers():
+    """Keys and values that are not numbers, and junk behind the last token, in a prompt's tiles: they
+    reach the rows that see them, a value only in its block's dimensions."""
+    _case("attention prompt nan")
+    g = np.random.default_rng(15)
+    for which in (0, 1):
+        b = Batch(g, 1, 64, 16, [120, 75])
+        news = [100, 75]
+        slot = b.slots(0)[46]  # seen by the tokens from 46 on: rows 26 .. 99 of the request
+        _, _, sc = b.lay.offsets(int(slot), which)
+        b.data[sc[0, 32]], b.data[sc[0, 32] + 1] = 0x00, 0x7E
+        good = Batch.__new__(Batch)
+        good.lay, good.lens = b.lay, [46, 75]
+        good.rows = lambda r, b=b: tuple(x[:good.lens[r]] for x in b.rows(r))
+        for t in TYPES:
+            q, q64 = rounded(g.standard_normal((175, 2, 64)), t)
+            out, lse = run_attention(b, q, news)
+            hit = out[26:100, :, 32:] if which else out[26:100]
+            assert np.isnan(hit).all()
+            if which:
+                assert np.isfinite(out[26:100, :, :32]).all() and np.isfinite(lse).all()
+            keep = list(range(26)) + list(range(100, 175))
+            check_attention(good, q64[keep], out[keep], lse[keep], [26, 75], t, 64**-0.5, 0)
+
+
+def test_attention_prompt_pages_outside_the_cache():
+    _case("attention prompt bad pages")
+    g = np.random.default_rng(16)
+    b = Batch(g, 2, 128, 16, [100, 64])
+    rows = [b.rows(r) for r in range(2)]
+    hidden = [np.zeros(n, bool) for n in b.lens]
+    for r, col, page in ((0, 1, -1), (0, 4, b.pages), (0, 5, 10**6), (1, 0, 2**31 - 1)):
+        b.table[r, col] = page
+        hidden[r][16 * col:16 * col + 16] = True
+    b.rows = lambda r: rows[r]
+    news = [60, 64]
+    for t in TYPES:
+        q, q64 = rounded(g.standard_normal((124, 4, 128)), t)
+        out, lse = run_attention(b, q, news)
+        check_attention(b, q64, out, lse, news, t, 128**-0.5, 0, hidden=lambda r: hidden[r])
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+def test_attention_prompt_rows_behind(t):
+    """Prompts beside single tokens and requests without tokens; rows behind the last one and an output
+    with strides are left alone; the same call gives the same bits."""
+    _case("attention prompt rows", t)
+    g = np.random.default_rng(18)
+    b = Batch(g, 2, 64, 32, [0, 140, 55, 2, 64])
+    news = [0, 90, 1, 4, 64]
+    q, q64 = rounded(g.standard_normal((sum(news) + 5, 8, 64)), t)
+    outs = []
+    for _ in range(3):
+        wide = torch.full((sum(news) + 5, 10, 64), 5.0, dtype=TYPES[t], device="cuda:0")
+        got, lse = run_attention(b, q, news, out=wide[:, 1:9])
+        assert bool((wide[:, 0] == 5).all()) and bool((wide[:, 9] == 5).all()) and (got[sum(news):] == 5).all()
+        outs.append(wide)
+    assert all(torch.equal(outs[0], o) for o in outs)
+    check_attention(b, q64, got, lse, news, t, 64**-0.5, 0)
+
+
 def test_attention_query_that_is_not_a_number():
     _case("attention nan query")
     g = np.random.default_rng(6)
