@@ -45,7 +45,10 @@ constexpr float kSlack = 2.f;    // see step()
 // A request with more query columns a kv head (new tokens x heads) than this goes to k_kv_wide, if
 // that is launched: from an average of as many a request. TODO
 constexpr int kWideCols = 32;
-constexpr int kWideGrid = 2 * kComputeUnits;
+#ifndef KV_WGRID
+#define KV_WGRID 2
+#endif
+constexpr int kWideGrid = KV_WGRID * kComputeUnits;
 
 bool split_type(int type) { return type != TQ_BF16; }
 
@@ -725,8 +728,8 @@ struct Attn {
 
 // A workgroup takes 64 CT query columns, 16 CT a wave. Each wave unpacks a quarter of a step (one
 // tile of keys or of values) into LDS in the matrix cores' operand layout, so a nibble is unpacked
-// once for 64 CT columns, and all waves read all of it. Two stages: a step is unpacked while the
-// step before it is multiplied, one barrier a step; raw quants are on their way two steps ahead.
+// once for 64 CT columns, and all waves read all of it. Two stages and one barrier a step: behind it,
+// a wave unpacks its part of the next step, asks for the raw quants of the one after, and multiplies.
 // Bound by vector issue, so the values' scales are applied where it costs least: for bf16
 // activations to the values, once, as they are unpacked (rounded to fp16, 2^-12 of a value, against
 // 2^-9 in the output; a tile's values are brought to [0, 8) by a power of two, which the softmax
@@ -743,25 +746,23 @@ struct Wide {
   static constexpr int kQueryTerms = sizeof(T) == 4 ? 2 : 1;  // fp16 and bf16 queries are one term
   // offsets in a stage: key operands, value operands, scales, then what Header holds
   static constexpr int kValues = 2048 * NB, kScales = 4096 * NB, kHeader = 4224 * NB;
-  static constexpr int kStage = kHeader + 32;
+  static constexpr int kStage = kHeader + 128;
   static constexpr int kLds = 2 * kStage;
 
   struct Header {  // of a step's two tiles
+    int exponent[2][4];   // the values of tokens 4 g + 0..3 are stored times 2^-exponent
+    uint32_t odd[2][4];   // a scale among them is no number
     uint32_t no_page[2];  // the tile's page is outside the cache
-    uint32_t odd[2];      // a scale of its values is no number
-    int exponent[2];      // its values are stored times 2^-exponent
-    int unused[2];
   };
 
   struct Raw {
-    uint32_t q[NB], s;  // the lane's share of a tile's key or value quants; a dword of its scales
+    uint32_t q[NB], s[2 * NB];  // the lane's share of a tile's key or value quants, its tokens' scales
     uint32_t no_page;
   };
 
   static __device__ __forceinline__ void load(const uint8_t *p, int lane, Raw &r) {
     typedef __attribute__((address_space(1))) const u32x2 *g2;
     typedef __attribute__((address_space(1))) const u32x3a4 *g3;
-    typedef __attribute__((address_space(1))) const uint32_t *g1;
     if constexpr (NB == 2) {
       const u32x2 w = *(g2)(p + lane * 8);
       r.q[0] = w[0];
@@ -778,15 +779,34 @@ struct Wide {
         for (int i = 0; i < 4; ++i) r.q[4 * c + i] = w[i];
       }
     }
-    r.s = lane < 8 * NB ? *(g1)(p + 256 * NB + lane * 4) : 0u;
+    p += 256 * NB + (lane >> 4) * 8 * NB;
+    if constexpr (NB % 2 == 0) {
+#pragma unroll
+      for (int c = 0; c < NB / 2; ++c) {
+        const u32x4 w = gload(p + 16 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.s[4 * c + i] = w[i];
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < NB; ++c) {
+        const u32x2 w = *(g2)(p + 8 * c);
+        r.s[2 * c] = w[0];
+        r.s[2 * c + 1] = w[1];
+      }
+    }
   }
 
   // Tile i of the step as operands into a stage.
-  static __device__ __forceinline__ void unpack_into(uint8_t *stage, bool values, int i, int lane, Raw &r) {
+  static __device__ __forceinline__ void unpack_into(uint8_t *stage, bool values, int i, int lane, const Raw &r) {
     const Unpack uk;
+    const int g = lane >> 4;
     Header *head = (Header *)(stage + kHeader);
-    uint8_t *scales = stage + kScales + ((values ? 2 : 0) + i) * 32 * NB;
-    if (lane < 8 * NB) *(uint32_t *)(scales + lane * 4) = r.s;
+    if ((lane & 15) == 0) {
+      uint8_t *to = stage + kScales + ((values ? 2 : 0) + i) * 32 * NB + g * 8 * NB;
+#pragma unroll
+      for (int c = 0; c < NB; ++c) *(u32x2 *)(to + 8 * c) = u32x2{r.s[2 * c], r.s[2 * c + 1]};
+    }
     if (!values) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -799,21 +819,20 @@ struct Wide {
     }
     f16x2 d[2 * NB];
     if constexpr (!SPLIT) {
-      uint32_t raw[2 * NB];  // (this wave's own store above)
-      read_scales<NB>(scales, lane >> 4, raw);
       typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+      uint32_t raw[2 * NB];
       auto exponent = [&]() {
         u16x2 most = {0, 0};
 #pragma unroll
         for (int j = 0; j < 2 * NB; ++j)
           most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, raw[j] & 0x7C007C00u));
-        int top = max((int)most[0], (int)most[1]) >> 10;
-        top = max(top, __shfl_xor(top, 16));
-        return __builtin_amdgcn_readfirstlane(max(top, __shfl_xor(top, 32)));
+        return max((int)most[0], (int)most[1]) >> 10;
       };
+#pragma unroll
+      for (int j = 0; j < 2 * NB; ++j) raw[j] = r.s[j];
       int top = exponent();
       const bool odd = top == 31;
-      if (odd) {  // not numbers as 0 here, and the columns that see them afterwards: see_odd()
+      if (__any(odd)) {  // not numbers as 0 here, and the columns that see them afterwards: see_odd()
 #pragma unroll
         for (int j = 0; j < 2 * NB; ++j) {
           if ((raw[j] & 0x7C00u) == 0x7C00u) raw[j] &= 0xFFFF0000u;
@@ -825,9 +844,9 @@ struct Wide {
       const _Float16 f = (_Float16)ldexpf(1.f, -e);
 #pragma unroll
       for (int j = 0; j < 2 * NB; ++j) d[j] = __builtin_bit_cast(f16x2, raw[j]) * f16x2{f, f};
-      if (lane == 0) {
-        head->odd[i] = odd;
-        head->exponent[i] = e;
+      if ((lane & 15) == 0) {
+        head->odd[i][g] = odd;
+        head->exponent[i][g] = e;
       }
     }
 #pragma unroll
@@ -937,7 +956,7 @@ struct Wide {
                                                        int lane, State<NB, CT> &st, int (&odd)[CT]) {
     const int g = lane >> 4;
     const Header *head = (const Header *)(stage + kHeader);
-    const float e[2] = {(float)head->exponent[0], (float)head->exponent[1]};
+    const float e[2] = {(float)head->exponent[0][g], (float)head->exponent[1][g]};
     const float back[2] = {__builtin_amdgcn_exp2f(-e[0]), __builtin_amdgcn_exp2f(-e[1])};
     bool move = false;
     float want[CT];
@@ -988,7 +1007,7 @@ struct Wide {
         st.o[c][2 * b + 1] = mfma(w[c], v1, st.o[c][2 * b + 1]);
       }
     }
-    if (__builtin_amdgcn_readfirstlane(head->odd[0] | head->odd[1])) see_odd(stage, mask, lo, hi, t0, g, odd);
+    if (__any(head->odd[0][g] | head->odd[1][g])) see_odd(stage, mask, lo, hi, t0, g, odd);
   }
 
   // Bit b of odd[c]: the lane's column sees one of the lane's tokens whose block b has a scale that is no
@@ -1035,17 +1054,19 @@ struct Wide {
       typedef __attribute__((address_space(4))) const int32_t *scalar;
       return ((scalar)(uintptr_t)table)[__builtin_amdgcn_readfirstlane(min(t >> a.g.page_shift, last_block))];
     };
-    auto fetch = [&](int i, Raw &r) {  // past the end the last step again
-      const int t = 32 * (from + min(i, steps - 1)) + 16 * half;
-      const int page = page_of(t);
+    auto token_of = [&](int i) { return 32 * (from + min(i, steps - 1)) + 16 * half; };  // past the end the last again
+    Raw raw;
+    int next_page = 0;
+    auto fetch = [&](int i) {
+      const int t = token_of(i), page = next_page;
+      next_page = page_of(token_of(i + 1));
       const int64_t ok = (unsigned)page < pages ? page : 0;
-      r.no_page = (unsigned)page >= pages;
-      load(head_data + ok * a.g.page_bytes + (int64_t)((t & (a.g.page_tokens - 1)) >> 4) * a.g.tile_bytes, lane, r);
+      raw.no_page = (unsigned)page >= pages;
+      load(head_data + ok * a.g.page_bytes + (int64_t)((t & (a.g.page_tokens - 1)) >> 4) * a.g.tile_bytes, lane, raw);
     };
-    Raw raw0, raw1;
     if (steps > 0) {
-      fetch(0, raw0);
-      fetch(1, raw1);
+      next_page = page_of(token_of(0));
+      fetch(0);
     }
     f16x8 qf[CT][kQueryTerms][NB];
     float qs[CT];
@@ -1083,12 +1104,19 @@ struct Wide {
     State<NB, CT> st;
     st.clear();
     int odd[CT] = {};
-    auto turn = [&](int i, Raw &r, uint8_t *stage) {
-      unpack_into(stage, values, half, lane, r);
-      fetch(i + 2, r);
+    if (steps > 0) {
+      unpack_into(lds, values, half, lane, raw);
+      fetch(1);
+    }
+    for (int i = 0; i < steps; ++i) {
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      uint8_t *stage = lds + (i & 1) * kStage;
+      if (i + 1 < steps) {
+        unpack_into(lds + kStage - (i & 1) * kStage, values, half, lane, raw);
+        fetch(i + 2);
+      }
       const int t0 = 32 * (from + i);
-      if (mine <= 0 || t0 >= mine_hi || t0 + 32 <= mine_lo) return;
+      if (mine <= 0 || t0 >= mine_hi || t0 + 32 <= mine_lo) continue;
       const Header *head = (const Header *)(stage + kHeader);
       const bool bad0 = __builtin_amdgcn_readfirstlane(head->no_page[0]), bad1 = __builtin_amdgcn_readfirstlane(head->no_page[1]);
       const bool inner = t0 >= all_lo && t0 + 32 <= all_hi && !bad0 && !bad1;
@@ -1100,10 +1128,6 @@ struct Wide {
         hi1[c] = min(hi[c], h0);
       }
       step(stage, qf, qs, !inner, lo1, hi1, max(mine_lo, l0), min(mine_hi, h0), t0, lane, st, odd);
-    };
-    for (int i = 0; i < steps; i += 2) {
-      turn(i, raw0, lds);
-      if (i + 1 < steps) turn(i + 1, raw1, lds + kStage);
     }
     const int l16 = lane & 15;
 #pragma unroll
@@ -1191,8 +1215,11 @@ __global__ __launch_bounds__(kThreads, resident(NB)) void k_kv_attn(AttnArgs a) 
 
 // Bound by vector issue: 32 scale products, 8 exponentials and 32 weights a lane for 16 matrix
 // products of 16 columns.
+#ifndef KV_WOCC
+#define KV_WOCC 2
+#endif
 template <typename A, int NB, bool SPLIT>
-__global__ __launch_bounds__(kThreads, 2) void k_kv_wide(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, KV_WOCC) void k_kv_wide(AttnArgs a) {
   extern __shared__ __align__(16) uint8_t attn_lds[];
   take_share<Wide<A, NB, SPLIT>>(a, attn_lds);
 }
