@@ -729,7 +729,7 @@ struct Attn {
 // A workgroup takes 64 CT query columns, 16 CT a wave. Each wave unpacks a quarter of a step (one
 // tile of keys or of values) into LDS in the matrix cores' operand layout, so a nibble is unpacked
 // once for 64 CT columns, and all waves read all of it. Two stages and one barrier a step: behind it,
-// a wave unpacks its part of the next step, asks for the raw quants of the one after, and multiplies.
+// a wave unpacks its part of the next step, asks for the raw quants of the second after it, and multiplies.
 // Bound by vector issue, so the values' scales are applied where it costs least: for bf16
 // activations to the values, once, as they are unpacked (rounded to fp16, 2^-12 of a value, against
 // 2^-9 in the output; a tile's values are brought to [0, 8) by a power of two, which the softmax
@@ -1055,9 +1055,9 @@ struct Wide {
       return ((scalar)(uintptr_t)table)[__builtin_amdgcn_readfirstlane(min(t >> a.g.page_shift, last_block))];
     };
     auto token_of = [&](int i) { return 32 * (from + min(i, steps - 1)) + 16 * half; };  // past the end the last again
-    Raw raw;
+    Raw raw0, raw1;
     int next_page = 0;
-    auto fetch = [&](int i) {
+    auto fetch = [&](int i, Raw &raw) {
       const int t = token_of(i), page = next_page;
       next_page = page_of(token_of(i + 1));
       const int64_t ok = (unsigned)page < pages ? page : 0;
@@ -1066,7 +1066,8 @@ struct Wide {
     };
     if (steps > 0) {
       next_page = page_of(token_of(0));
-      fetch(0);
+      fetch(0, raw0);
+      fetch(1, raw1);
     }
     f16x8 qf[CT][kQueryTerms][NB];
     float qs[CT];
@@ -1105,18 +1106,18 @@ struct Wide {
     st.clear();
     int odd[CT] = {};
     if (steps > 0) {
-      unpack_into(lds, values, half, lane, raw);
-      fetch(1);
+      unpack_into(lds, values, half, lane, raw0);
+      fetch(2, raw0);
     }
-    for (int i = 0; i < steps; ++i) {
+    auto turn = [&](int i, Raw &raw) {  // raw: of step i + 1
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       uint8_t *stage = lds + (i & 1) * kStage;
       if (i + 1 < steps) {
         unpack_into(lds + kStage - (i & 1) * kStage, values, half, lane, raw);
-        fetch(i + 2);
+        fetch(i + 3, raw);
       }
       const int t0 = 32 * (from + i);
-      if (mine <= 0 || t0 >= mine_hi || t0 + 32 <= mine_lo) continue;
+      if (mine <= 0 || t0 >= mine_hi || t0 + 32 <= mine_lo) return;
       const Header *head = (const Header *)(stage + kHeader);
       const bool bad0 = __builtin_amdgcn_readfirstlane(head->no_page[0]), bad1 = __builtin_amdgcn_readfirstlane(head->no_page[1]);
       const bool inner = t0 >= all_lo && t0 + 32 <= all_hi && !bad0 && !bad1;
@@ -1128,6 +1129,10 @@ struct Wide {
         hi1[c] = min(hi[c], h0);
       }
       step(stage, qf, qs, !inner, lo1, hi1, max(mine_lo, l0), min(mine_hi, h0), t0, lane, st, odd);
+    };
+    for (int i = 0; i < steps; i += 2) {
+      turn(i, raw1);
+      if (i + 1 < steps) turn(i + 1, raw0);
     }
     const int l16 = lane & 15;
 #pragma unroll
