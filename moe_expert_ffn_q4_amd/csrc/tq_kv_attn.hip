@@ -31,24 +31,17 @@ constexpr int kThreads = 64 * kWaves;
 // 128 and 256); a full launch has just as many, all of them resident at once.
 constexpr int resident(int nb) { return nb <= 4 ? 3 : 2; }
 constexpr int kComputeUnits = 256;
-#ifndef KV_ITEM
-#define KV_ITEM 16
-#endif
-#ifndef KV_MIN
-#define KV_MIN 8
-#endif
-constexpr int kMinUnits = KV_MIN;     // units per workgroup at least
-constexpr int kItemUnits = KV_ITEM;    // what an item costs beside its steps (queries, merge, output)
+constexpr int kMinUnits = 8;  // units per workgroup at least
+// What an item costs beside its steps (queries, merge, output), in steps of k_kv_attn and k_kv_wide.
+constexpr int item_units(bool wide) { return wide ? 5 : 16; }
 constexpr float kLowest = -3.4028234663852886e38f;
 constexpr float kSlack = 2.f;    // see step()
 
 // A request with more query columns a kv head (new tokens x heads) than this goes to k_kv_wide, if
 // that is launched: from an average of as many a request. TODO
 constexpr int kWideCols = 32;
-#ifndef KV_WGRID
-#define KV_WGRID 2
-#endif
-constexpr int kWideGrid = KV_WGRID * kComputeUnits;
+// Workgroups of k_kv_wide per compute unit (registers: 256 a lane up to head_dim 128, 512 for 256).
+constexpr int resident_wide(int nb) { return nb <= 4 ? 2 : 1; }
 
 bool split_type(int type) { return type != TQ_BF16; }
 
@@ -56,7 +49,7 @@ bool wide_launch(int64_t group, int64_t rows, int64_t requests) { return rows * 
 
 // ---- the step's work as one line of units -----------------------------------------------------
 // An item is a query tile (up to NCOL columns: tokens x heads of one kv head) of a request; its
-// units are the 32-token steps of its request and kItemUnits for what it costs beside them. All
+// units are the 32-token steps of its request and item_units for what it costs beside them. All
 // items' units form one line, cut into equal shares, one a workgroup, so ragged batches load the
 // chip evenly; a share of an item's units is the same share of its steps. The lengths live on the
 // device, so every workgroup forms the prefix sums over the requests itself.
@@ -93,7 +86,7 @@ __device__ __forceinline__ Request request(const AttnArgs &a, const TileShape &t
   q.first_pos = q.len - q.fresh;
   const bool wide = (int64_t)q.fresh * a.group > a.wide_cols;
   q.tiles = wide == WIDE ? (q.fresh + ts.tokens - 1) / ts.tokens * ts.splits : 0;
-  q.units = kItemUnits + max(0, (q.len + 31) / 32 - seen_from(a, q.first_pos) / 32);
+  q.units = item_units(WIDE) + max(0, (q.len + 31) / 32 - seen_from(a, q.first_pos) / 32);
   return q;
 }
 
@@ -886,25 +879,38 @@ struct Wide {
                                               State<NB, CT> &st, int (&odd)[CT]) {
     const int g = lane >> 4;
     float s[CT][8];
+    // Software pipeline, kept by the scheduling barriers (left alone, the compiler reads, waits,
+    // multiplies and waits again, operand by operand): the operands of kRead products ahead are
+    // read, and a product's results are scaled while the next ones are multiplied.
+    constexpr int kProducts = 2 * NB, kRead = kQueryTerms == 2 ? 2 : 4;
+    uint32_t ks[2][2 * NB];
+    f16x8 k[kProducts];
+    f32x4 d[2][CT];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t ks[2 * NB];
-      read_scales<NB>(stage + kScales + i * 32 * NB, g, ks);
+    for (int i = 0; i < 2; ++i) read_scales<NB>(stage + kScales + i * 32 * NB, g, ks[i]);
 #pragma unroll
-      for (int c = 0; c < CT; ++c)
+    for (int n = 0; n < kRead; ++n) k[n] = *(const f16x8 *)(stage + n * 1024 + lane * 16);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s[c][4 * i + r] = 0.f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const f16x8 k = *(const f16x8 *)(stage + (i * NB + b) * 1024 + lane * 16);
+    for (int n = 0; n <= kProducts; ++n) {  // product n: tile n / NB, block n % NB
+      if (n < kProducts) {
+        if (n + kRead < kProducts) k[n + kRead] = *(const f16x8 *)(stage + (n + kRead) * 1024 + lane * 16);
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+          d[n & 1][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int t = kQueryTerms - 1; t >= 0; --t) d = mfma(k, qf[c][t][b], d);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s[c][4 * i + r] = fmaf(scale_of(ks, b, r), d[r], s[c][4 * i + r]);
+          for (int t = kQueryTerms - 1; t >= 0; --t) d[n & 1][c] = mfma(k[n], qf[c][t][n % NB], d[n & 1][c]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (n > 0) {
+        const int i = (n - 1) / NB, b = (n - 1) % NB;
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            s[c][4 * i + r] = fmaf(scale_of(ks[i], b, r), d[(n - 1) & 1][c][r], b ? s[c][4 * i + r] : 0.f);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     if (mask) {
@@ -956,7 +962,11 @@ struct Wide {
                                                        int lane, State<NB, CT> &st, int (&odd)[CT]) {
     const int g = lane >> 4;
     const Header *head = (const Header *)(stage + kHeader);
+    f16x8 v[2 * NB];  // read before the softmax
+#pragma unroll
+    for (int j = 0; j < 2 * NB; ++j) v[j] = *(const f16x8 *)(stage + kValues + j * 1024 + lane * 16);
     const float e[2] = {(float)head->exponent[0][g], (float)head->exponent[1][g]};
+    __builtin_amdgcn_sched_barrier(0);
     const float back[2] = {__builtin_amdgcn_exp2f(-e[0]), __builtin_amdgcn_exp2f(-e[1])};
     bool move = false;
     float want[CT];
@@ -998,15 +1008,9 @@ struct Wide {
       }
     }
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const f16x8 v0 = *(const f16x8 *)(stage + kValues + 2 * b * 1024 + lane * 16);
-      const f16x8 v1 = *(const f16x8 *)(stage + kValues + (2 * b + 1) * 1024 + lane * 16);
+    for (int j = 0; j < 2 * NB; ++j)
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        st.o[c][2 * b] = mfma(w[c], v0, st.o[c][2 * b]);
-        st.o[c][2 * b + 1] = mfma(w[c], v1, st.o[c][2 * b + 1]);
-      }
-    }
+      for (int c = 0; c < CT; ++c) st.o[c][j] = mfma(w[c], v[j], st.o[c][j]);
     if (__any(head->odd[0][g] | head->odd[1][g])) see_odd(stage, mask, lo, hi, t0, g, odd);
   }
 
@@ -1220,26 +1224,25 @@ __global__ __launch_bounds__(kThreads, resident(NB)) void k_kv_attn(AttnArgs a) 
 
 // Bound by vector issue: 32 scale products, 8 exponentials and 32 weights a lane for 16 matrix
 // products of 16 columns.
-#ifndef KV_WOCC
-#define KV_WOCC 2
-#endif
 template <typename A, int NB, bool SPLIT>
-__global__ __launch_bounds__(kThreads, KV_WOCC) void k_kv_wide(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, resident_wide(NB)) void k_kv_wide(AttnArgs a) {
   extern __shared__ __align__(16) uint8_t attn_lds[];
   take_share<Wide<A, NB, SPLIT>>(a, attn_lds);
 }
 
 // Workgroup (w, y) joins the item whose first part workgroup w of k_kv_attn left: part 2 w + 1 and
-// the parts 2 w' of the following workgroups. A thread takes four dimensions of a column and every
-// fourth part. Bound by latency: the parts' references, sums and outputs are read eight parts at a
-// time, at once.
-constexpr int kJoinUnits = 128, kJoinGroups = 4;
+// the parts 2 w' of the following workgroups. A thread takes four dimensions of a column and, of
+// k_kv_attn's parts (up to hundreds of a long sequence), every fourth; k_kv_wide's items have few
+// parts. Bound by latency: the parts' references, sums and outputs are read eight parts at a time,
+// at once.
+constexpr int kJoinThreads = 512;
 
 template <typename X>
-__global__ __launch_bounds__(kJoinUnits * kJoinGroups) void k_kv_join(AttnArgs a) {
+__global__ __launch_bounds__(kJoinThreads) void k_kv_join(AttnArgs a) {
+  constexpr int kJoinGroups = X::kWide ? 1 : 4, kJoinUnits = kJoinThreads / kJoinGroups;
   constexpr int kRuns = X::D / 4, kBatch = 8;
-  __shared__ f32x4 other_o[kJoinGroups - 1][kJoinUnits];
-  __shared__ float other_m[kJoinGroups - 1][kJoinUnits], other_l[kJoinGroups - 1][kJoinUnits];
+  __shared__ f32x4 other_o[kJoinGroups][kJoinUnits];
+  __shared__ float other_m[kJoinGroups][kJoinUnits], other_l[kJoinGroups][kJoinUnits];
   const int w = blockIdx.x, unit = threadIdx.x % kJoinUnits, group = threadIdx.x / kJoinUnits;
   const int i = blockIdx.y * kJoinUnits + unit;
   const JoinItem item = ((const JoinItem *)a.joins)[w];
@@ -1274,15 +1277,17 @@ __global__ __launch_bounds__(kJoinUnits * kJoinGroups) void k_kv_join(AttnArgs a
       join(pm[k], pl[k], po[k]);
     }
   }
-  if (group > 0) {
-    other_m[group - 1][unit] = m;
-    other_l[group - 1][unit] = l;
-    other_o[group - 1][unit] = o;
+  if constexpr (kJoinGroups > 1) {
+    if (group > 0) {
+      other_m[group][unit] = m;
+      other_l[group][unit] = l;
+      other_o[group][unit] = o;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   if (group > 0 || !live) return;
 #pragma unroll
-  for (int k = 0; k < kJoinGroups - 1; ++k) join(other_m[k][unit], other_l[k][unit], other_o[k][unit]);
+  for (int k = 1; k < kJoinGroups; ++k) join(other_m[k][unit], other_l[k][unit], other_o[k][unit]);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     store_out<typename X::Act>(a, item.row, item.head0, item.per, c, d + j, l == 0.f ? 0.f : o[j] / l);
@@ -1308,9 +1313,9 @@ int launch_class(const AttnArgs &args, int grid, hipStream_t s) {
     }
   }
   K<<<dim3(grid), kThreads, X::kLds, s>>>(a);
-  constexpr int kUnits = X::NCOL * X::D / 4;  // units of an item
+  constexpr int kThreadsOfItem = X::NCOL * X::D / 4 * (X::kWide ? 1 : 4);
   if (grid > 1)
-    k_kv_join<X><<<dim3(grid - 1, (kUnits + kJoinUnits - 1) / kJoinUnits), kJoinUnits * kJoinGroups, 0, s>>>(a);
+    k_kv_join<X><<<dim3(grid - 1, (kThreadsOfItem + kJoinThreads - 1) / kJoinThreads), kJoinThreads, 0, s>>>(a);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
@@ -1320,7 +1325,7 @@ int launch(const AttnArgs &args, hipStream_t s) {
   const bool wide = wide_launch(a.group, a.rows, a.requests);
   a.wide_cols = wide ? kWideCols : INT32_MAX;
   if (wide) {
-    const int rc = launch_class<Wide<A, NB, SPLIT>, k_kv_wide<A, NB, SPLIT>>(a, kWideGrid, s);
+    const int rc = launch_class<Wide<A, NB, SPLIT>, k_kv_wide<A, NB, SPLIT>>(a, kComputeUnits * resident_wide(NB), s);
     if (rc) return rc;
   }
   return launch_class<Attn<A, NB, SPLIT>, k_kv_attn<A, NB, SPLIT>>(a, a.grid, s);
@@ -1343,7 +1348,8 @@ size_t kv_attention_workspace(int type, int64_t head_dim, int64_t group, int64_t
     return (size_t)(workgroups * (2 * columns * (head_dim + 2) * 4 + (int64_t)sizeof(JoinItem)));
   };
   const size_t few = bytes(grid, split_type(type) ? 8 : 16);
-  const size_t many = wide_launch(group, rows, requests) ? bytes(kWideGrid, head_dim == 256 ? 64 : 128) : 0;
+  const size_t many = wide_launch(group, rows, requests)
+                          ? bytes(kComputeUnits * resident_wide((int)(head_dim / 32)), head_dim == 256 ? 64 : 128) : 0;
   return few > many ? few : many;
 }
 
@@ -1351,7 +1357,7 @@ int kv_attention_grid(int type, int64_t kv_heads, int64_t head_dim, int64_t grou
   // an upper bound of the units: every row a tile of its own over the longest sequence
   const int64_t ncol = split_type(type) ? 8 : 16;
   const int64_t tiles = rows * (group <= ncol ? 1 : (group + ncol - 1) / ncol);
-  const int64_t steps = max_len / 32 + 2 + kItemUnits;
+  const int64_t steps = max_len / 32 + 2 + item_units(false);
   const double units = (double)tiles * (double)kv_heads * (double)steps;
   const double most = units / kMinUnits + 1;
   const int full = kComputeUnits * resident((int)(head_dim / 32));
