@@ -157,23 +157,57 @@ __global__ __launch_bounds__(kThreads) void k_kv_plan(PlanArgs a) {
 
 // ---- append ---------------------------------------------------------------------------------
 
+// W pairs of a head turned by cosine and sine t[0..W): runs e0 and e1 of W elements each; interleaved:
+// the runs follow each other and hold the pairs side by side. In T's arithmetic.
+template <typename F, typename C, int W>
+__device__ __forceinline__ void turn_pairs(F (&lo)[W], F (&hi)[W], const C *t, bool interleaved) {
+  if (interleaved) {
+    F v[2 * W];
+#pragma unroll
+    for (int k = 0; k < 2 * W; ++k) v[k] = k < W ? lo[k] : hi[k - W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const F x0 = v[2 * k], x1 = v[2 * k + 1], c = t[k].x, s = t[k].y;
+      v[2 * k] = x0 * c - x1 * s;
+      v[2 * k + 1] = x0 * s + x1 * c;
+    }
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      lo[k] = v[k];
+      hi[k] = v[W + k];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const F x0 = lo[k], x1 = hi[k], c = t[k].x, s = t[k].y;
+      lo[k] = x0 * c - x1 * s;
+      hi[k] = x0 * s + x1 * c;
+    }
+  }
+}
+
 // One workgroup: `rb` rows x `hg` kv heads (and their share of the q heads). The rows' sines and
 // cosines are formed once per workgroup in fp64 (an fp32 angle is off by 0.03 rad at position
-// 500000) and kept in LDS; q heads go from global memory to global memory, k and v heads into LDS
-// as fp32, from where sixteen lanes round a block of 32 (lane c holds its values c and c + 16, the
-// two nibbles of one byte). W pairs are turned per thread step.
-template <typename A, int W>
+// 500000) and kept in LDS. Keys are turned in fp64 and rounded to fp32 once, so that the 4-bit
+// rounding that follows is the definition's; queries, of which there are several times as many, are
+// turned in fp32 (fp64 conversions and products took half of the kernel's time: 120 us for 8192 rows
+// of 64 + 16 heads). q heads go from global memory to global memory, k and v heads into LDS as fp32,
+// from where sixteen lanes round a block of 32 (lane c holds its values c and c + 16, the two
+// nibbles of one byte). W pairs are turned per thread step, 16 bytes of a run where the rows allow.
+template <typename A, int W, int NB>
 __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a, int rb, int hg) {
   typedef typename A::type T;
+  constexpr int D = 32 * NB, kUnits = D / (2 * W);  // thread steps per head
   extern __shared__ double2 append_lds[];
   __shared__ int slot_lds[16];
-  const int tid = threadIdx.x, D = a.head_dim, pairs = a.inv_freq ? a.pairs : 0;
+  const int tid = threadIdx.x, pairs = a.inv_freq ? a.pairs : 0;
   const int row0 = blockIdx.x * rb, rows = min(rb, a.rows - row0);
   const int h0 = blockIdx.y * hg, heads = min(hg, a.g.heads - h0);
   const int q0 = (int)((int64_t)a.q.heads * blockIdx.y / gridDim.y);
   const int qn = (int)((int64_t)a.q.heads * (blockIdx.y + 1) / gridDim.y) - q0;
-  double2 *turn = append_lds;                                // [rb][pairs]: cosine, sine
-  float *stage = (float *)(append_lds + (int64_t)rb * pairs);  // [rb][k heads, v heads][D]
+  double2 *turn = append_lds;                      // [rb][pairs]: cosine, sine
+  float2 *turn32 = (float2 *)(turn + rb * pairs);  // the same in fp32
+  float *stage = (float *)(turn32 + ((rb * pairs + 1) & ~1));  // [rb][k heads, v heads][D]
   if (tid < rows) {
     const int slot = a.slots[row0 + tid];
     slot_lds[tid] = slot >= 0 && (slot >> a.g.page_shift) < a.g.pages ? slot : -1;
@@ -188,93 +222,73 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a, int rb, in
     double si, co;
     sincos(angle, &si, &co);
     turn[i] = make_double2(co, si);
+    turn32[i] = make_float2((float)co, (float)si);
   }
   __syncthreads();
-  const int units = D / (2 * W);  // thread steps per head
-  const int per_row = qn + 2 * heads;
-  for (int i = tid; i < rows * per_row * units; i += kThreads) {
-    const int u = i % units, rest = i / units, row = rest / per_row, j = rest - row * per_row;
+  // the two runs of W elements of a head's step u: W pairs, or 2 W elements that stay
+  auto runs = [&](int u, int np, int &e0, int &e1) {
+    const bool turned = u * W < np;
+    e0 = turned ? (a.interleaved ? 2 * u * W : u * W) : 2 * np + (u * W - np) * 2;
+    e1 = e0 + (turned && !a.interleaved ? np : W);
+    return turned;
+  };
+  for (int i = tid; i < rows * 2 * heads * kUnits; i += kThreads) {
+    const int u = i % kUnits, rest = i / kUnits, row = rest / (2 * heads), j = rest - row * 2 * heads;
     if (slot_lds[row] < 0) continue;
-    const bool is_q = j < qn, is_v = j >= qn + heads;
-    const int head = is_q ? q0 + j : h0 + j - qn - (is_v ? heads : 0);
-    const T *x = (const T *)(is_q ? a.q.data : is_v ? a.v.data : a.k.data) +
-                 (row0 + row) * (is_q ? a.q.row_stride : is_v ? a.v.row_stride : a.k.row_stride) +
-                 head * (is_q ? a.q.head_stride : is_v ? a.v.head_stride : a.k.head_stride);
-    // the two runs of W elements that this step takes, W pairs or 2 W elements that stay
-    const bool turned = !is_v && u * W < pairs;
+    const bool is_v = j >= heads;
+    const int head = h0 + (is_v ? j - heads : j);
+    const T *x = (const T *)(is_v ? a.v.data : a.k.data) +
+                 (row0 + row) * (is_v ? a.v.row_stride : a.k.row_stride) + head * (is_v ? a.v.head_stride : a.k.head_stride);
     int e0, e1;
-    if (turned && !a.interleaved) {
-      e0 = u * W;
-      e1 = e0 + pairs;
-    } else if (!is_v && !turned) {  // past the turned ones
-      e0 = 2 * pairs + (u * W - pairs) * 2;
-      e1 = e0 + W;
-    } else {
-      e0 = 2 * u * W;
-      e1 = e0 + W;
-    }
+    const bool turned = runs(u, is_v ? 0 : pairs, e0, e1);
     float lo[W], hi[W];
     load_run<A, W, (W > 1)>(x + e0, lo);
     load_run<A, W, (W > 1)>(x + e1, hi);
-    double dlo[W], dhi[W];
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      dlo[k] = lo[k];
-      dhi[k] = hi[k];
-    }
     if (turned) {
-      const double2 *t = turn + row * pairs + u * W;
-      if (a.interleaved) {
-        double v[2 * W];
-#pragma unroll
-        for (int k = 0; k < 2 * W; ++k) v[k] = k < W ? dlo[k] : dhi[k - W];
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-          const double x0 = v[2 * k], x1 = v[2 * k + 1], c = t[k].x, s = t[k].y;
-          v[2 * k] = x0 * c - x1 * s;
-          v[2 * k + 1] = x0 * s + x1 * c;
-        }
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-          dlo[k] = v[k];
-          dhi[k] = v[W + k];
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-          const double x0 = dlo[k], x1 = dhi[k], c = t[k].x, s = t[k].y;
-          dlo[k] = x0 * c - x1 * s;
-          dhi[k] = x0 * s + x1 * c;
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      lo[k] = (float)dlo[k];
-      hi[k] = (float)dhi[k];
-    }
-    if (is_q) {
-      T *y = (T *)a.q_out.data + (row0 + row) * a.q_out.row_stride + head * a.q_out.head_stride;
-      store_run<A, W, (W > 1)>(y + e0, lo);
-      store_run<A, W, (W > 1)>(y + e1, hi);
-    } else {
-      float *y = stage + ((int64_t)row * 2 * heads + (j - qn)) * D;
+      double dlo[W], dhi[W];
 #pragma unroll
       for (int k = 0; k < W; ++k) {
-        y[e0 + k] = lo[k];
-        y[e1 + k] = hi[k];
+        dlo[k] = lo[k];
+        dhi[k] = hi[k];
+      }
+      turn_pairs<double, double2, W>(dlo, dhi, turn + row * pairs + u * W, a.interleaved);
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        lo[k] = (float)dlo[k];
+        hi[k] = (float)dhi[k];
       }
     }
+    float *y = stage + (row * 2 * heads + j) * D;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      y[e0 + k] = lo[k];
+      y[e1 + k] = hi[k];
+    }
+  }
+  for (int i = tid; i < rows * qn * kUnits; i += kThreads) {
+    const int u = i % kUnits, rest = i / kUnits, row = rest / qn, head = q0 + rest - row * qn;
+    if (slot_lds[row] < 0) continue;
+    const T *x = (const T *)a.q.data + (row0 + row) * a.q.row_stride + head * a.q.head_stride;
+    T *y = (T *)a.q_out.data + (row0 + row) * a.q_out.row_stride + head * a.q_out.head_stride;
+    int e0, e1;
+    const bool turned = runs(u, pairs, e0, e1);
+    float lo[W], hi[W];
+    load_run<A, W, (W > 1)>(x + e0, lo);
+    load_run<A, W, (W > 1)>(x + e1, hi);
+    if (turned) turn_pairs<float, float2, W>(lo, hi, turn32 + row * pairs + u * W, a.interleaved);
+    store_run<A, W, (W > 1)>(y + e0, lo);
+    store_run<A, W, (W > 1)>(y + e1, hi);
   }
   __syncthreads();
-  const int nb = a.g.nb, blocks = rows * 2 * heads * nb;
+  constexpr int nb = NB;
+  const int blocks = rows * 2 * heads * nb;
   const int lane = tid & 63, c = lane & 15, wave = wave_index();
   for (int i0 = wave * 4; i0 < blocks; i0 += kThreads / 16) {
     const int i = min(i0 + (lane >> 4), blocks - 1);  // the ballots below take whole waves
     const int b = i % nb, rest = i / nb, j = rest % (2 * heads), row = rest / (2 * heads);
     const int slot = slot_lds[row];
     const bool live = slot >= 0 && i == i0 + (lane >> 4);
-    const float *x = stage + ((int64_t)row * 2 * heads + j) * D + 32 * b;
+    const float *x = stage + (row * 2 * heads + j) * D + 32 * b;
     const float lo = slot >= 0 ? x[c] : 0.f, hi = slot >= 0 ? x[c + 16] : 0.f;
     const bool odd = !(fabsf(lo) < INFINITY) || !(fabsf(hi) < INFINITY);
     float most = fmaxf(fabsf(lo), fabsf(hi));
@@ -320,87 +334,108 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a, int rb, in
 
 // ---- read -----------------------------------------------------------------------------------
 
-// One thread: four neighbouring values of each half of a block (one dword of key quants, or one
-// byte from each of four dwords of value quants).
-template <typename A>
-__global__ __launch_bounds__(kThreads) void k_kv_read(ReadArgs a) {
+// One thread: eight neighbouring values of each half of a block of one row and head (two dwords of
+// key quants, or a byte from each of eight dwords of value quants), in 16-byte stores. Bound by HBM
+// on the outputs; four tokens share the dwords of value quants, and rows of a workgroup that follow
+// each other find them in the cache.
+template <typename A, int NB>
+__global__ __launch_bounds__(kThreads) void k_kv_read(ReadArgs a, int rows_per_wg) {
   typedef typename A::type T;
-  const int nb = a.g.nb, per_head = nb * 4;
-  const int64_t per_row = (int64_t)a.g.heads * per_head, n = a.rows * per_row;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= n) return;
-  const int row = (int)(i / per_row), in = (int)(i - row * per_row);
-  const int h = in / per_head, u = in - h * per_head, b = u >> 2, f = u & 3;
-  const int slot = a.slots[row];
-  const bool there = slot >= 0 && (slot >> a.g.page_shift) < a.g.pages;
-  const uint8_t *tile = a.g.data + (there ? tile_of_slot(a.g, slot, h) : 0);
-  const int tok = slot & 15, scale_at = ((tok >> 2) * nb + b) * 4 + (tok & 3);
-  const int64_t out = ((int64_t)row * a.g.heads + h) * a.head_dim + 32 * b + 4 * f;
-  auto give = [&](void *dst, const uint32_t byte[4], float d) {
-    float lo[4], hi[4];
+  constexpr int kUnits = NB * 2, kWords = NB < 4 ? NB : 4;
+  const int per_row = a.g.heads * kUnits, row0 = blockIdx.x * rows_per_wg;
+  const int n = min(rows_per_wg, a.rows - row0) * per_row;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int u = i % kUnits, rest = i / kUnits, r = rest / a.g.heads, h = rest - r * a.g.heads;
+    const int row = row0 + r, b = u >> 1, f = u & 1;
+    const int slot = a.slots[row];
+    const bool there = slot >= 0 && (slot >> a.g.page_shift) < a.g.pages;
+    const uint8_t *tile = a.g.data + (there ? tile_of_slot(a.g, slot, h) : 0);
+    const int tok = there ? slot & 15 : 0, scale_at = ((tok >> 2) * NB + b) * 4 + (tok & 3);
+    const int64_t out = ((int64_t)row * a.g.heads + h) * (32 * NB) + 32 * b + 8 * f;
+    const int chunk = b / kWords, word = b - chunk * kWords;
+    auto give = [&](void *dst, const uint32_t (&byte)[8], float d) {
+      float lo[8], hi[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      lo[k] = there ? d * (float)((int)(byte[k] & 15u) - 8) : 0.f;
-      hi[k] = there ? d * (float)((int)(byte[k] >> 4) - 8) : 0.f;
-    }
-    store_run<A, 4, true>((T *)dst + out, lo);
-    store_run<A, 4, true>((T *)dst + out + 16, hi);
-  };
-  if (a.k) {
-    uint32_t byte[4] = {0, 0, 0, 0};
-    float d = 0.f;
-    if (there) {
-      const uint32_t w = ((const uint32_t *)tile)[quant_word(a.g, b, f, tok)];
-      d = (float)((const _Float16 *)(tile + a.g.quant_bytes))[scale_at];
+      for (int k = 0; k < 8; ++k) {
+        lo[k] = there ? d * (float)((int)(byte[k] & 15u) - 8) : 0.f;
+        hi[k] = there ? d * (float)((int)(byte[k] >> 4) - 8) : 0.f;
+      }
+      store_run<A, 8, true>((T *)dst + out, lo);
+      store_run<A, 8, true>((T *)dst + out + 16, hi);
+    };
+    uint32_t byte[8];
+    if (a.k) {
+      const uint32_t *quants = (const uint32_t *)tile + ((chunk * 4 + 2 * f) * 16 + tok) * kWords + word;
+      const uint32_t w0 = quants[0], w1 = quants[16 * kWords];
+      const float d = (float)((const _Float16 *)(tile + 256 * NB))[scale_at];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) byte[k] = (w >> (8 * quant_place(k))) & 0xFFu;
+      for (int k = 0; k < 8; ++k) byte[k] = ((k < 4 ? w0 : w1) >> (8 * quant_place(k))) & 0xFFu;
+      give(a.k, byte, d);
     }
-    give(a.k, byte, d);
-  }
-  if (a.v) {
-    uint32_t byte[4] = {0, 0, 0, 0};
-    float d = 0.f;
-    if (there) {
-      tile += a.g.half_bytes;
-      d = (float)((const _Float16 *)(tile + a.g.quant_bytes))[scale_at];
+    if (a.v) {
+      tile += 288 * NB;
+      const float d = (float)((const _Float16 *)(tile + 256 * NB))[scale_at];
+      const uint8_t *quants = tile + 4 * (((chunk * 4 + (tok >> 2)) * 16 + 8 * f) * kWords + word) + quant_place(tok);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        byte[k] = tile[4 * quant_word(a.g, b, tok >> 2, 4 * f + k) + quant_place(tok)];
+      for (int k = 0; k < 8; ++k) byte[k] = quants[4 * kWords * k];
+      give(a.v, byte, d);
     }
-    give(a.v, byte, d);
   }
 }
 
-template <typename A>
+template <typename A, int NB>
 int launch_append(const AppendArgs &a, hipStream_t s) {
+  constexpr int kRun = 16 / (int)sizeof(typename A::type);  // elements of a 16-byte run
   const int pairs = a.inv_freq ? a.pairs : 0;
+  auto lds = [&](int rb, int hg) { return rb * (pairs * 24 + 16 + 2 * hg * a.head_dim * 4); };
   // few rows: one row and head per workgroup (latency); many: four rows share the sines of eight
   // heads, within 60 KB of LDS
   int rb = 1, hg = 1;
   if ((int64_t)a.rows * a.g.heads > 1024) {
     rb = 4;
     hg = 8;
-    while (hg > 1 && rb * (pairs * 16 + 2 * hg * a.head_dim * 4) > 60 * 1024) hg >>= 1;
+    while (hg > 1 && lds(rb, hg) > 60 * 1024) hg >>= 1;
   }
   hg = hg < a.g.heads ? hg : a.g.heads;
-  const size_t lds = (size_t)rb * (pairs * 16 + 2 * hg * a.head_dim * 4);
   const dim3 grid((a.rows + rb - 1) / rb, (a.g.heads + hg - 1) / hg);
   auto fits = [](const HeadRows &h) {
-    return h.data == nullptr || (((uintptr_t)h.data % (4 * sizeof(typename A::type))) == 0 &&
-                                 h.row_stride % 4 == 0 && h.head_stride % 4 == 0);
+    return h.data == nullptr || ((uintptr_t)h.data % 16 == 0 && h.row_stride % kRun == 0 && h.head_stride % kRun == 0);
   };
-  if (pairs % 4 == 0 && fits(a.k) && fits(a.v) && fits(a.q) && fits(a.q_out))
-    k_kv_append<A, 4><<<grid, kThreads, lds, s>>>(a, rb, hg);
+  if (pairs % kRun == 0 && fits(a.k) && fits(a.v) && fits(a.q) && fits(a.q_out))
+    k_kv_append<A, kRun, NB><<<grid, kThreads, lds(rb, hg), s>>>(a, rb, hg);
   else
-    k_kv_append<A, 1><<<grid, kThreads, lds, s>>>(a, rb, hg);
+    k_kv_append<A, 1, NB><<<grid, kThreads, lds(rb, hg), s>>>(a, rb, hg);
+  return launch_status();
+}
+
+template <typename A, int NB>
+int launch_read(const ReadArgs &a, hipStream_t s) {
+  // few rows: a workgroup per row; many: enough rows for each thread to take four units
+  const int per_row = a.g.heads * NB * 2;
+  const int most = (4 * kThreads + per_row - 1) / per_row;
+  const int rows = clampi(a.rows / 1024, 1, most);
+  k_kv_read<A, NB><<<dim3((a.rows + rows - 1) / rows), kThreads, 0, s>>>(a, rows);
   return launch_status();
 }
 
 template <typename A>
-int launch_read(const ReadArgs &a, hipStream_t s) {
-  const int64_t n = (int64_t)a.rows * a.g.heads * a.g.nb * 4;
-  k_kv_read<A><<<dim3((unsigned)((n + kThreads - 1) / kThreads)), kThreads, 0, s>>>(a);
-  return launch_status();
+int append_dim(const AppendArgs &a, hipStream_t s) {
+  switch (a.g.nb) {
+    case 2: return launch_append<A, 2>(a, s);
+    case 3: return launch_append<A, 3>(a, s);
+    case 4: return launch_append<A, 4>(a, s);
+    default: return launch_append<A, 8>(a, s);
+  }
+}
+
+template <typename A>
+int read_dim(const ReadArgs &a, hipStream_t s) {
+  switch (a.g.nb) {
+    case 2: return launch_read<A, 2>(a, s);
+    case 3: return launch_read<A, 3>(a, s);
+    case 4: return launch_read<A, 4>(a, s);
+    default: return launch_read<A, 8>(a, s);
+  }
 }
 
 }  // namespace
@@ -413,13 +448,13 @@ int launch_kv_plan(const PlanArgs &a, hipStream_t s) {
 }
 
 int launch_kv_append(int type, const AppendArgs &a, hipStream_t s) {
-  return type == TQ_F32 ? launch_append<ActF32>(a, s)
-         : type == TQ_BF16 ? launch_append<ActBF16>(a, s) : launch_append<ActF16>(a, s);
+  return type == TQ_F32 ? append_dim<ActF32>(a, s)
+         : type == TQ_BF16 ? append_dim<ActBF16>(a, s) : append_dim<ActF16>(a, s);
 }
 
 int launch_kv_read(int type, const ReadArgs &a, hipStream_t s) {
-  return type == TQ_F32 ? launch_read<ActF32>(a, s)
-         : type == TQ_BF16 ? launch_read<ActBF16>(a, s) : launch_read<ActF16>(a, s);
+  return type == TQ_F32 ? read_dim<ActF32>(a, s)
+         : type == TQ_BF16 ? read_dim<ActBF16>(a, s) : read_dim<ActF16>(a, s);
 }
 
 }  // namespace tq
