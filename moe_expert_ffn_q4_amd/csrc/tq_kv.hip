@@ -157,6 +157,18 @@ __global__ __launch_bounds__(kThreads) void k_kv_plan(PlanArgs a) {
 
 // ---- append ---------------------------------------------------------------------------------
 
+// v of the lane N to the right within its row of 16 (rotating), without LDS.
+template <int N>
+__device__ __forceinline__ float row_rotate(float v) {
+  const int i = __builtin_bit_cast(int, v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, 0x120 + N, 0xF, 0xF, false));
+}
+// v of lane ^ N (1 or 2).
+template <int N>
+__device__ __forceinline__ uint32_t quad_swap(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, N == 1 ? 0xB1 : 0x4E, 0xF, 0xF, false);
+}
+
 // W pairs of a head turned by cosine and sine t[0..W): runs e0 and e1 of W elements each; interleaved:
 // the runs follow each other and hold the pairs side by side. In T's arithmetic.
 template <typename F, typename C, int W>
@@ -280,75 +292,102 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a, int rb, in
     store_run<A, W, (W > 1)>(y + e1, hi);
   }
   __syncthreads();
-  constexpr int nb = NB;
-  const int blocks = rows * 2 * heads * nb;
-  const int lane = tid & 63, c = lane & 15, wave = wave_index();
-  for (int i0 = wave * 4; i0 < blocks; i0 += kThreads / 16) {
-    const int i = min(i0 + (lane >> 4), blocks - 1);  // the ballots below take whole waves
-    const int b = i % nb, rest = i / nb, j = rest % (2 * heads), row = rest / (2 * heads);
+  // a group of sixteen lanes takes a row's head, block by block
+  const int lane = tid & 63, c = lane & 15, sh = lane & 48, pairs_of = rows * 2 * heads;
+  for (int i0 = wave_index() * 4; i0 < pairs_of; i0 += kThreads / 16) {
+    const int i = min(i0 + (lane >> 4), pairs_of - 1);  // the ballots below take whole waves
+    const int row = i / (2 * heads), j = i - row * 2 * heads;
     const int slot = slot_lds[row];
-    const bool live = slot >= 0 && i == i0 + (lane >> 4);
-    const float *x = stage + (row * 2 * heads + j) * D + 32 * b;
-    const float lo = slot >= 0 ? x[c] : 0.f, hi = slot >= 0 ? x[c + 16] : 0.f;
-    const bool odd = !(fabsf(lo) < INFINITY) || !(fabsf(hi) < INFINITY);
-    float most = fmaxf(fabsf(lo), fabsf(hi));
-    for (int d = 1; d < 16; d <<= 1) most = fmaxf(most, __shfl_xor(most, d));
-    const int sh = lane & 48;
-    auto group = [&](bool v) { return (unsigned)(__ballot(v) >> sh) & 0xFFFFu; };
-    const unsigned in_lo = group(fabsf(lo) == most), in_hi = group(fabsf(hi) == most);
-    const unsigned neg_lo = group(lo < 0.f), neg_hi = group(hi < 0.f), any_odd = group(odd);
-    // sign of the first value of largest magnitude: values 0..15 are the lo ones
-    const bool negative = in_lo ? (neg_lo >> __builtin_ctz(in_lo)) & 1
-                                : in_hi ? (neg_hi >> __builtin_ctz(in_hi)) & 1 : false;
-    const float want = fminf(most * 0.125f, 65504.f);
-    _Float16 d = (_Float16)(negative ? want : -want);
-    if (any_odd) d = __builtin_bit_cast(_Float16, (uint16_t)0x7E00);
-    const float df = (float)d, inv = 1.f / df;
-    // nearest even of v / d, exactly: v - n d is exact in fp32 (n has 4 bits, d 11), so its
-    // comparison with d / 2 settles what the rounded reciprocal may have missed
-    auto nibble = [&](float v) -> uint32_t {
-      if (any_odd || df == 0.f) return 8u;
-      float n = fminf(fmaxf(rintf(v * inv), -9.f), 9.f);
-      const float r = fmaf(-n, df, v), h = 0.5f * fabsf(df);
-      const float toward = (r < 0.f) == (df < 0.f) ? 1.f : -1.f;  // the neighbour on r's side
-      const float m = n + toward;
-      if (fabsf(r) > h || (fabsf(r) == h && ((int)n & 1))) n = m;
-      return (uint32_t)(8 + (int)fminf(fmaxf(n, -8.f), 7.f));
-    };
-    const uint32_t byte = nibble(lo) | nibble(hi) << 4;
-    const int h = h0 + (j < heads ? j : j - heads), tok = slot & 15;
-    const bool is_v = j >= heads;
-    uint8_t *tile = a.g.data + (slot >= 0 ? tile_of_slot(a.g, slot, h) : 0) + (is_v ? a.g.half_bytes : 0);
-    uint32_t word = byte << (8 * quant_place(c));
-    word |= __shfl_xor(word, 1);
-    word |= __shfl_xor(word, 2);
-    if (!live) continue;
-    if (!is_v) {
-      if ((c & 3) == 0) ((uint32_t *)tile)[quant_word(a.g, b, c >> 2, tok)] = word;
-    } else {
-      tile[4 * quant_word(a.g, b, tok >> 2, c) + quant_place(tok)] = (uint8_t)byte;
+    const bool live = slot >= 0 && i == i0 + (lane >> 4), is_v = j >= heads;
+    const int tok = slot & 15;
+    const float *x = stage + (row * 2 * heads + j) * D;
+    uint8_t *tile = a.g.data + (live ? tile_of_slot(a.g, slot, h0 + (is_v ? j - heads : j)) : 0) + (is_v ? 288 * NB : 0);
+    // the lane's byte of value quants, or (every fourth lane) its dword of key quants, of block 0
+    constexpr int kWords = NB < 4 ? NB : 4;
+    uint8_t *to = tile + (is_v ? ((tok >> 2) * 16 + c) * kWords * 4 + quant_place(tok) : ((c >> 2) * 16 + tok) * kWords * 4);
+    _Float16 *to_scale = (_Float16 *)(tile + 256 * NB) + (tok >> 2) * NB * 4 + (tok & 3);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const float lo = slot >= 0 ? x[32 * b + c] : 0.f, hi = slot >= 0 ? x[32 * b + c + 16] : 0.f;
+      float most = fmaxf(fabsf(lo), fabsf(hi));
+      const bool odd = !(fabsf(lo) < INFINITY) || !(fabsf(hi) < INFINITY);
+      most = fmaxf(most, row_rotate<8>(most));
+      most = fmaxf(most, row_rotate<4>(most));
+      most = fmaxf(most, row_rotate<2>(most));
+      most = fmaxf(most, row_rotate<1>(most));
+      auto group = [&](bool v) { return (unsigned)(__ballot(v) >> sh) & 0xFFFFu; };
+      const unsigned in_lo = group(fabsf(lo) == most), in_hi = group(fabsf(hi) == most);
+      const unsigned neg_lo = group(lo < 0.f), neg_hi = group(hi < 0.f), any_odd = group(odd);
+      // sign of the first value of largest magnitude: values 0..15 are the lo ones
+      const unsigned in = in_lo ? in_lo : in_hi, neg = in_lo ? neg_lo : neg_hi;
+      const bool negative = (neg & in & (0u - in)) != 0;
+      const float want = fminf(most * 0.125f, 65504.f);
+      _Float16 d = (_Float16)(negative ? want : -want);
+      if (any_odd) d = __builtin_bit_cast(_Float16, (uint16_t)0x7E00);
+      const float df = (float)d, inv = __builtin_amdgcn_rcpf(df), h = 0.5f * fabsf(df);
+      const bool none = any_odd || df == 0.f;
+      // nearest even of v / d, exactly: v - n d is exact in fp32 (n has 4 bits, d 11), so its
+      // comparison with d / 2 settles what the approximate reciprocal may have missed
+      auto nibble = [&](float v) -> uint32_t {
+        float n = fminf(fmaxf(rintf(v * inv), -9.f), 9.f);
+        const float r = fmaf(-n, df, v);
+        const float m = n + ((r < 0.f) == (df < 0.f) ? 1.f : -1.f);  // the neighbour on r's side
+        if (fabsf(r) > h || (fabsf(r) == h && ((int)n & 1))) n = m;
+        return none ? 8u : (uint32_t)(8 + (int)fminf(fmaxf(n, -8.f), 7.f));
+      };
+      const uint32_t byte = nibble(lo) | nibble(hi) << 4;
+      uint32_t word = byte << (8 * quant_place(c));
+      word |= quad_swap<1>(word);
+      word |= quad_swap<2>(word);
+      if (!live) continue;
+      constexpr int kChunk = 64 * kWords * 4;
+      uint8_t *at = to + (b / kWords) * kChunk + (b % kWords) * 4;
+      if (is_v) *at = (uint8_t)byte;
+      else if ((c & 3) == 0) *(uint32_t *)at = word;
+      if (c == 0) to_scale[4 * b] = d;
     }
-    if (c == 0) ((_Float16 *)(tile + a.g.quant_bytes))[((tok >> 2) * nb + b) * 4 + (tok & 3)] = d;
   }
 }
 
 // ---- read -----------------------------------------------------------------------------------
 
-// One thread: eight neighbouring values of each half of a block of one row and head (two dwords of
-// key quants, or a byte from each of eight dwords of value quants), in 16-byte stores. Bound by HBM
-// on the outputs; four tokens share the dwords of value quants, and rows of a workgroup that follow
-// each other find them in the cache.
+// One thread: eight neighbouring values of each half of a block of one row and head, in 16-byte
+// stores. Value quants (a byte of each of sixteen dwords that four tokens share) come through LDS,
+// fetched 16 bytes a lane: read byte by byte from global memory, the loads' address work took the
+// whole time (66 cycles an instruction; 119 us for 65536 rows).
 template <typename A, int NB>
 __global__ __launch_bounds__(kThreads) void k_kv_read(ReadArgs a, int rows_per_wg) {
   typedef typename A::type T;
-  constexpr int kUnits = NB * 2, kWords = NB < 4 ? NB : 4;
-  const int per_row = a.g.heads * kUnits, row0 = blockIdx.x * rows_per_wg;
-  const int n = min(rows_per_wg, a.rows - row0) * per_row;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int u = i % kUnits, rest = i / kUnits, r = rest / a.g.heads, h = rest - r * a.g.heads;
-    const int row = row0 + r, b = u >> 1, f = u & 1;
+  constexpr int kUnits = NB * 2, kWords = NB < 4 ? NB : 4, kHeads = kThreads / kUnits, kPieces = NB * 4;
+  __shared__ u32x4 quads[kHeads][kPieces + 1];  // a row's head: the dwords of its four tokens' value quants
+  const int row0 = blockIdx.x * rows_per_wg;
+  const int n = min(rows_per_wg, a.rows - row0) * a.g.heads;  // heads of rows
+  auto place = [&](int i, int &row, int &h, bool &there) {
+    const int r = i / a.g.heads;
+    row = row0 + r;
+    h = i - r * a.g.heads;
     const int slot = a.slots[row];
-    const bool there = slot >= 0 && (slot >> a.g.page_shift) < a.g.pages;
+    there = slot >= 0 && (slot >> a.g.page_shift) < a.g.pages;
+    return slot;
+  };
+  for (int i0 = 0; i0 < n; i0 += kHeads) {
+    const int here = min(kHeads, n - i0);
+    int row, h;
+    bool there;
+    if (a.v) {
+      if (i0) __syncthreads();
+      for (int p = threadIdx.x; p < here * kPieces; p += kThreads) {
+        const int slot = place(i0 + p / kPieces, row, h, there), q = p % kPieces;
+        constexpr int kChunk = kWords * 4;  // pieces of a chunk
+        if (there)
+          quads[p / kPieces][q] = gload(a.g.data + tile_of_slot(a.g, slot, h) + 288 * NB +
+                                        ((q / kChunk * 4 + ((slot & 15) >> 2)) * kChunk + q % kChunk) * 16);
+      }
+      __syncthreads();
+    }
+    const int u = threadIdx.x % kUnits, mine = threadIdx.x / kUnits;
+    if (mine >= here) continue;
+    const int slot = place(i0 + mine, row, h, there), b = u >> 1, f = u & 1;
     const uint8_t *tile = a.g.data + (there ? tile_of_slot(a.g, slot, h) : 0);
     const int tok = there ? slot & 15 : 0, scale_at = ((tok >> 2) * NB + b) * 4 + (tok & 3);
     const int64_t out = ((int64_t)row * a.g.heads + h) * (32 * NB) + 32 * b + 8 * f;
@@ -373,9 +412,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(ReadArgs a, int rows_per_w
       give(a.k, byte, d);
     }
     if (a.v) {
-      tile += 288 * NB;
-      const float d = (float)((const _Float16 *)(tile + 256 * NB))[scale_at];
-      const uint8_t *quants = tile + 4 * (((chunk * 4 + (tok >> 2)) * 16 + 8 * f) * kWords + word) + quant_place(tok);
+      const float d = (float)((const _Float16 *)(tile + 544 * NB))[scale_at];
+      const uint8_t *quants = (const uint8_t *)&quads[mine][0] + 4 * ((chunk * 16 + 8 * f) * kWords + word) + quant_place(tok);
 #pragma unroll
       for (int k = 0; k < 8; ++k) byte[k] = quants[4 * kWords * k];
       give(a.v, byte, d);
