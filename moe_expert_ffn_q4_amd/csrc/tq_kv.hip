@@ -351,72 +351,64 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a, int rb, in
 
 // ---- read -----------------------------------------------------------------------------------
 
-// One thread: eight neighbouring values of each half of a block of one row and head, in 16-byte
-// stores. Value quants (a byte of each of sixteen dwords that four tokens share) come through LDS,
-// fetched 16 bytes a lane: read byte by byte from global memory, the loads' address work took the
-// whole time (66 cycles an instruction; 119 us for 65536 rows).
+// One thread: eight neighbouring values of one row and head, keys and values, so that a wave stores
+// whole lines. The quants (of a value row: a byte of each of sixteen dwords a block, which four
+// tokens share) come through LDS, fetched 16 bytes a lane: read byte by byte from global memory, the
+// loads' address work took the whole time (66 cycles an instruction; 119 us for 65536 rows).
 template <typename A, int NB>
 __global__ __launch_bounds__(kThreads) void k_kv_read(ReadArgs a, int rows_per_wg) {
   typedef typename A::type T;
-  constexpr int kUnits = NB * 2, kWords = NB < 4 ? NB : 4, kHeads = kThreads / kUnits, kPieces = NB * 4;
+  constexpr int kUnits = NB * 4, kWords = NB < 4 ? NB : 4, kHeads = kThreads / kUnits, kPieces = NB * 4;
   __shared__ u32x4 quads[kHeads][kPieces + 1];  // a row's head: the dwords of its four tokens' value quants
+  __shared__ uint32_t keys[kHeads][kPieces + 1];  // its key quants [chunk][i / 4][word]
   const int row0 = blockIdx.x * rows_per_wg;
   const int n = min(rows_per_wg, a.rows - row0) * a.g.heads;  // heads of rows
-  auto place = [&](int i, int &row, int &h, bool &there) {
-    const int r = i / a.g.heads;
-    row = row0 + r;
-    h = i - r * a.g.heads;
-    const int slot = a.slots[row];
-    there = slot >= 0 && (slot >> a.g.page_shift) < a.g.pages;
-    return slot;
-  };
+  const int u = threadIdx.x % kUnits, mine = threadIdx.x / kUnits;  // also the piece that the thread fetches
+  const int b = u >> 2, half = u >> 1 & 1, f = u & 1;
+  const int chunk = b / kWords, word = b - chunk * kWords;
   for (int i0 = 0; i0 < n; i0 += kHeads) {
-    const int here = min(kHeads, n - i0);
-    int row, h;
-    bool there;
-    if (a.v) {
-      if (i0) __syncthreads();
-      for (int p = threadIdx.x; p < here * kPieces; p += kThreads) {
-        const int slot = place(i0 + p / kPieces, row, h, there), q = p % kPieces;
+    const int i = i0 + mine;
+    const bool live = mine < kHeads && i < n;
+    const int r = live ? i / a.g.heads : 0, row = row0 + r, h = live ? i - r * a.g.heads : 0;
+    const int slot = a.slots[row], tok = slot & 15;
+    const bool there = slot >= 0 && (slot >> a.g.page_shift) < a.g.pages;
+    float kd = 0.f, vd = 0.f;
+    if (i0) __syncthreads();
+    if (live && there) {
+      const uint8_t *tile = a.g.data + tile_of_slot(a.g, slot, h);
+      const int scale_at = ((tok >> 2) * NB + b) * 4 + (tok & 3);
+      if (a.k) {
+        keys[mine][u] = ((const uint32_t *)tile)[(u / kWords * 16 + tok) * kWords + u % kWords];
+        kd = (float)((const _Float16 *)(tile + 256 * NB))[scale_at];
+      }
+      if (a.v) {
         constexpr int kChunk = kWords * 4;  // pieces of a chunk
-        if (there)
-          quads[p / kPieces][q] = gload(a.g.data + tile_of_slot(a.g, slot, h) + 288 * NB +
-                                        ((q / kChunk * 4 + ((slot & 15) >> 2)) * kChunk + q % kChunk) * 16);
+        quads[mine][u] = gload(tile + 288 * NB + ((u / kChunk * 4 + (tok >> 2)) * kChunk + u % kChunk) * 16);
+        vd = (float)((const _Float16 *)(tile + 544 * NB))[scale_at];
       }
-      __syncthreads();
     }
-    const int u = threadIdx.x % kUnits, mine = threadIdx.x / kUnits;
-    if (mine >= here) continue;
-    const int slot = place(i0 + mine, row, h, there), b = u >> 1, f = u & 1;
-    const uint8_t *tile = a.g.data + (there ? tile_of_slot(a.g, slot, h) : 0);
-    const int tok = there ? slot & 15 : 0, scale_at = ((tok >> 2) * NB + b) * 4 + (tok & 3);
-    const int64_t out = ((int64_t)row * a.g.heads + h) * (32 * NB) + 32 * b + 8 * f;
-    const int chunk = b / kWords, word = b - chunk * kWords;
+    __syncthreads();
+    if (!live) continue;
+    const int64_t out = ((int64_t)row * a.g.heads + h) * (32 * NB) + 8 * u;
     auto give = [&](void *dst, const uint32_t (&byte)[8], float d) {
-      float lo[8], hi[8];
+      float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        lo[k] = there ? d * (float)((int)(byte[k] & 15u) - 8) : 0.f;
-        hi[k] = there ? d * (float)((int)(byte[k] >> 4) - 8) : 0.f;
-      }
-      store_run<A, 8, true>((T *)dst + out, lo);
-      store_run<A, 8, true>((T *)dst + out + 16, hi);
+      for (int k = 0; k < 8; ++k) v[k] = there ? d * (float)((int)(byte[k] >> (4 * half) & 15u) - 8) : 0.f;
+      store_run<A, 8, true>((T *)dst + out, v);
     };
     uint32_t byte[8];
     if (a.k) {
-      const uint32_t *quants = (const uint32_t *)tile + ((chunk * 4 + 2 * f) * 16 + tok) * kWords + word;
-      const uint32_t w0 = quants[0], w1 = quants[16 * kWords];
-      const float d = (float)((const _Float16 *)(tile + 256 * NB))[scale_at];
+      const uint32_t *q = &keys[mine][(chunk * 4 + 2 * f) * kWords + word];
+      const uint32_t w0 = q[0], w1 = q[kWords];
 #pragma unroll
       for (int k = 0; k < 8; ++k) byte[k] = ((k < 4 ? w0 : w1) >> (8 * quant_place(k))) & 0xFFu;
-      give(a.k, byte, d);
+      give(a.k, byte, kd);
     }
     if (a.v) {
-      const float d = (float)((const _Float16 *)(tile + 544 * NB))[scale_at];
-      const uint8_t *quants = (const uint8_t *)&quads[mine][0] + 4 * ((chunk * 16 + 8 * f) * kWords + word) + quant_place(tok);
+      const uint8_t *q = (const uint8_t *)&quads[mine][0] + 4 * ((chunk * 16 + 8 * f) * kWords + word) + quant_place(tok & 3);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) byte[k] = quants[4 * kWords * k];
-      give(a.v, byte, d);
+      for (int k = 0; k < 8; ++k) byte[k] = q[4 * kWords * k];
+      give(a.v, byte, vd);
     }
   }
 }
@@ -449,7 +441,7 @@ int launch_append(const AppendArgs &a, hipStream_t s) {
 template <typename A, int NB>
 int launch_read(const ReadArgs &a, hipStream_t s) {
   // few rows: a workgroup per row; many: enough rows for each thread to take four units
-  const int per_row = a.g.heads * NB * 2;
+  const int per_row = a.g.heads * NB * 4;
   const int most = (4 * kThreads + per_row - 1) / per_row;
   const int rows = clampi(a.rows / 1024, 1, most);
   k_kv_read<A, NB><<<dim3((a.rows + rows - 1) / rows), kThreads, 0, s>>>(a, rows);
