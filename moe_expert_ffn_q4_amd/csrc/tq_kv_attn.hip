@@ -490,31 +490,53 @@ struct Attn {
     const Unpack uk;
     const int g = lane >> 4;
     float s[1][8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t kq[NB], ks[2 * NB];
-      read_quants<NB>(at + i * kTile, lane, kq);
-      read_scales<NB>(at + i * kTile + kQuant, g, ks);
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint32_t n[4];
-        unpack(uk, kq[b], n);
-        const f32x4 d = mfma(join(n[0], n[1], n[2], n[3]), qf[b], f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] = fmaf(scale_of(ks, b, r), d[r], acc[r]);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float v = acc[r];
-        if constexpr (SPLIT) v += row_swap8(v);  // hi and lo columns of one query
-        s[0][4 * i + r] = v;
-      }
-      if constexpr (NB == 8) __builtin_amdgcn_sched_barrier(0);  // the tiles one by one: registers
-    }
+    // Software pipeline, kept by the scheduling barriers: everything the products need is read at
+    // once, and a product's results are scaled while the next one is multiplied.
+    constexpr int kTiles = NB == 8 ? 1 : 2;  // tiles read at once (registers)
     uint32_t vs[2][2 * NB];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) read_scales<NB>(at + i * kTile + kHalf + kQuant, g, vs[i]);
+    for (int i0 = 0; i0 < 2; i0 += kTiles) {
+      uint32_t kq[kTiles][NB], ks[kTiles][2 * NB];
+      f32x4 d[2];
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        read_quants<NB>(at + (i0 + i) * kTile, lane, kq[i]);
+        read_scales<NB>(at + (i0 + i) * kTile + kQuant, g, ks[i]);
+      }
+      if (kTiles == 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) read_scales<NB>(at + i * kTile + kHalf + kQuant, g, vs[i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n <= kTiles * NB; ++n) {  // product n: tile i0 + n / NB, block n % NB
+        if (n < kTiles * NB) {
+          uint32_t q[4];
+          unpack(uk, kq[n / NB][n % NB], q);
+          d[n & 1] = mfma(join(q[0], q[1], q[2], q[3]), qf[n % NB], f32x4{0.f, 0.f, 0.f, 0.f});
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (n > 0) {
+          const int i = (n - 1) / NB, b = (n - 1) % NB;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            s[0][4 * (i0 + i) + r] = fmaf(scale_of(ks[i], b, r), d[(n - 1) & 1][r], b ? s[0][4 * (i0 + i) + r] : 0.f);
+        }
+      }
+    }
+    uint32_t vq[2][NB];  // read before the softmax
+    if (kTiles == 2) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) read_quants<NB>(at + i * kTile + kHalf, lane, vq[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) read_scales<NB>(at + i * kTile + kHalf + kQuant, g, vs[i]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (SPLIT) {  // hi and lo columns of one query
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0][i] += row_swap8(s[0][i]);
+    }
     if (mask) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -527,9 +549,10 @@ struct Attn {
     const float qs1[1] = {qs};
     weigh<NB, 1>(s, qs1, vs, bits, g, st);
     const float (&p)[8] = s[0];
-    uint32_t vq[2][NB];
+    if (kTiles == 1) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) read_quants<NB>(at + i * kTile + kHalf, lane, vq[i]);
+      for (int i = 0; i < 2; ++i) read_quants<NB>(at + i * kTile + kHalf, lane, vq[i]);
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       f16x8 w;
