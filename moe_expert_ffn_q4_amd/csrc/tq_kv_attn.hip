@@ -451,6 +451,26 @@ __device__ __forceinline__ void store_lse(const AttnArgs &a, int row, int head0,
       l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
 }
 
+// A wave that is ahead steps back: priority 3 in the first quarter of the workgroup's share, then 2,
+// 1, 0. Issue goes to the oldest wave first: without it the first workgroups of a compute unit ended
+// after 31 us where the last took 50 us (k_kv_wide: 400 and 540), alone on their SIMDs at the end.
+struct StepBack {
+  int done, share, stride;  // units done before this segment, of the share; units from step to step
+  int level = 0, next = 0;
+
+  __device__ __forceinline__ void at(int i) {
+    if (i < next) return;
+    do {
+      if (level == 0) __builtin_amdgcn_s_setprio(3);
+      else if (level == 1) __builtin_amdgcn_s_setprio(2);
+      else if (level == 2) __builtin_amdgcn_s_setprio(1);
+      else __builtin_amdgcn_s_setprio(0);
+      ++level;
+      next = level >= 4 ? 0x7FFFFFFF : ((int)((int64_t)level * share / 4) - done) / stride;
+    } while (i >= next);
+  }
+};
+
 // ---- few columns: waves share an item's steps ----------------------------------------------------
 
 template <typename A, int NB, bool SPLIT>
@@ -589,19 +609,7 @@ struct Attn {
     st.clear();
     // the tile's own steps: the item's units are spread over them (a tile of early tokens has fewer)
     const int s0 = any_lo / 32, n = max(0, (any_hi + 31) / 32 - s0);
-    // A wave that is ahead steps back: priority 3 in the first quarter of the workgroup's share, then
-    // 2, 1, 0. (Issue goes to the oldest wave first: without it the first workgroups of a compute
-    // unit ended after 31 us where the last took 50 us, alone on their SIMDs at the end.)
-    int level = 0, next_level = 0;
-    auto step_back = [&](int i) {
-      if (i < next_level) return;
-      if (level == 0) __builtin_amdgcn_s_setprio(3);
-      else if (level == 1) __builtin_amdgcn_s_setprio(2);
-      else if (level == 2) __builtin_amdgcn_s_setprio(1);
-      else __builtin_amdgcn_s_setprio(0);
-      ++level;
-      next_level = level == 4 ? 0x7FFFFFFF : (level * share_units / 4 - done) / kWaves;
-    };
+    StepBack back{done, share_units, kWaves};
     const double share = (double)n / (double)q.units;  // exact where it has to be: 0 at 0, n at units
     auto step_at = [&](int v) { return s0 + (v == q.units ? n : (int)(v * share)); };
     const int from = step_at(v0), to = step_at(v1);
@@ -676,7 +684,7 @@ struct Attn {
       // the step that takes the place of the last one read, whose reads have all returned
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       const unsigned bad = bad_pages >> (2 * (i % (kAhead + 1))) & 3u;
-      step_back(i);
+      back.at(i);
       if (i + kAhead < steps) fetch(i + kAhead);
       wait_steps<NB, kAhead>(steps - 1 - i);
       const uint8_t *at = ring + (i % (kAhead + 1)) * Step<NB>::kBytes;
@@ -1055,8 +1063,7 @@ struct Wide {
   // The units [v0, v1) of an item, by the whole workgroup.
   static __device__ void segment(const AttnArgs &a, const TileShape &ts, const Request &q, int kvh, int tile,
                                  int v0, int v1, int done, int share_units, float *part, uint8_t *lds) {
-    (void)done;
-    (void)share_units;
+    StepBack back{done, share_units, 1};
     const int lane = threadIdx.x & 63, wave = wave_index(), g = lane >> 4;
     const Columns cs = columns<NCOL>(a, ts, q, kvh, tile);
     const int last_tok = cs.tok0 + (cs.count - 1) / cs.per;
@@ -1137,6 +1144,7 @@ struct Wide {
       fetch(2, raw0);
     }
     auto turn = [&](int i, Raw &raw) {  // raw: of step i + 1
+      back.at(i);
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       uint8_t *stage = lds + (i & 1) * kStage;
       if (i + 1 < steps) {
