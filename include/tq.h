@@ -488,10 +488,11 @@ int tq_kv_read(const tq_kv_cache *cache, int type, int64_t rows, const int32_t *
  * A row that sees no token gets out 0 and lse -inf. Rows outside cu_new[0] .. cu_new[requests] are
  * left as they were. fp32 sums and softmax; keys, values and queries enter the products exactly
  * (fp32 queries to 2^-22 of the row's largest), the softmax weights times the values' scales in
- * fp16 (TQ_BF16) or as two fp16 terms (TQ_F32, TQ_F16).
+ * fp16 (TQ_BF16) or as two fp16 terms (TQ_F32, TQ_F16). TQ_BF16 requests with many new tokens: the
+ * weights and the values each rounded to fp16. out must not overlap q or the cache.
  *   workspace: tq_kv_attention_workspace_bytes(...) bytes, 256-byte aligned, contents irrelevant;
  *   one call at a time per workspace. rows 0..2^20, requests 1..4096, q heads a multiple of
- *   kv_heads and at most 4096; max_blocks * page_tokens <= 2^30; scale > 0 and finite;
+ *   kv_heads and at most 4096; max_blocks * page_tokens <= 2^30; 0 < scale <= 1e30;
  *   0 <= window < 2^31. Deterministic.
  */
 typedef struct {

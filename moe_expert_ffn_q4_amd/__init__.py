@@ -552,8 +552,15 @@ class Rope:
                              (_i64 * 4)(*self.sections), int(interleaved))
 
 
-def _head_rows(t: torch.Tensor) -> HeadRows:
-    return HeadRows(t.data_ptr(), t.shape[1], t.stride(0), t.stride(1))
+def _head_rows(t: torch.Tensor, heads: int) -> HeadRows:
+    rows, head, _ = t.stride()
+    return HeadRows(t.data_ptr(), heads, rows, head)
+
+
+def _heads_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a tensor of rows, heads and head_dim")
+    return t.shape[1]
 
 
 def kv_plan(cache: KvCache, kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor,
@@ -566,10 +573,10 @@ def kv_plan(cache: KvCache, kv_len: torch.Tensor, new_len: torch.Tensor, block_t
     (int32; -1 in the rows after the last token), free_pages, free_count (the new one) and status
     [1], on the device: 0, or the sum of reasons why nothing was done (1 pages, 2 rows, 4 table
     columns, 8 lengths)."""
-    R, dev, i32 = kv_len.shape[0], cache.device, torch.int32
-    _kv_tensor(kv_len, "kv_len", i32, (None,), dev)
+    R, dev, i32 = kv_len.numel(), cache.device, torch.int32
+    _kv_tensor(kv_len, "kv_len", i32, (R,), dev)
     _kv_tensor(new_len, "new_len", i32, (R,), dev)
-    _kv_tensor(block_table, "block_table", i32, (R, None), dev)
+    _kv_tensor(block_table, "block_table", i32, (R, block_table.shape[-1]), dev)
     if (free_pages is None) != (free_count is None):
         raise ValueError("free_pages and free_count go together")
     if free_pages is not None:
@@ -613,8 +620,9 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     if not isinstance(k, torch.Tensor) or k.dtype not in ACT_TYPES:
         raise ValueError("k must be a tensor of fp32, bf16 or fp16")
     rows = k.shape[0]
-    _kv_tensor(k, "k", k.dtype, (rows, cache.kv_heads, D), dev, strided=True)
-    _kv_tensor(v, "v", k.dtype, (rows, cache.kv_heads, D), dev, strided=True)
+    shape = (rows, cache.kv_heads, D)
+    _kv_tensor(k, "k", k.dtype, shape, dev, True)
+    _kv_tensor(v, "v", k.dtype, shape, dev, True)
     _kv_tensor(slots, "slots", torch.int32, (rows,), dev)
     if (rope is None) != (positions is None):
         raise ValueError("rope and positions go together")
@@ -637,15 +645,18 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
             return kv_append(cache, k, v, slots, q, rope, positions, q_out)
     qr = orr = None
     if q is not None:
-        _kv_tensor(q, "q", k.dtype, (rows, None, D), dev, strided=True)
+        heads = _heads_of(q, "q")
+        shape = (rows, heads, D)
+        _kv_tensor(q, "q", k.dtype, shape, dev, True)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = torch.empty(shape, dtype=k.dtype, device=dev)
         else:
-            _kv_tensor(q_out, "q_out", k.dtype, q.shape, dev, strided=True)
-        qr, orr = C.byref(_head_rows(q)), C.byref(_head_rows(q_out))
+            _kv_tensor(q_out, "q_out", k.dtype, shape, dev, True)
+        qr, orr = C.byref(_head_rows(q, heads)), C.byref(_head_rows(q_out, heads))
     if rows:
         rc = lib().tq_kv_append(cache.ref, ACT_TYPES[k.dtype], rows, slots.data_ptr(),
-                                C.byref(_head_rows(k)), C.byref(_head_rows(v)), qr, orr,
+                                C.byref(_head_rows(k, cache.kv_heads)),
+                                C.byref(_head_rows(v, cache.kv_heads)), qr, orr,
                                 None if r is None else C.byref(r), _raw_stream(dev.index))
         if rc:
             _check(rc)
@@ -656,10 +667,10 @@ def kv_read(cache: KvCache, slots: torch.Tensor, dtype: torch.dtype = torch.floa
     """The keys and values at `slots` (int32 [rows]) as the values they stand for, two tensors
     [rows, kv_heads, head_dim] of `dtype` (tq_kv_read); zeros for slots outside the cache."""
     dev = cache.device
-    _kv_tensor(slots, "slots", torch.int32, (None,), dev)
+    _kv_tensor(slots, "slots", torch.int32, (slots.numel(),), dev)
     if dtype not in ACT_TYPES:
         raise ValueError("dtype must be fp32, bf16 or fp16")
-    rows = slots.shape[0]
+    rows = slots.numel()
     if _elsewhere(dev, stream):
         with _On(dev, stream):
             return kv_read(cache, slots, dtype)
@@ -685,13 +696,16 @@ def kv_attention(cache: KvCache, q: torch.Tensor, block_table: torch.Tensor, seq
     dev, D, i32 = cache.device, cache.head_dim, torch.int32
     if not isinstance(q, torch.Tensor) or q.dtype not in ACT_TYPES:
         raise ValueError("q must be a tensor of fp32, bf16 or fp16")
-    _kv_tensor(q, "q", q.dtype, (None, None, D), dev, strided=True)
-    rows, heads, _ = q.shape
+    heads = _heads_of(q, "q")
+    rows = q.shape[0]
+    shape = (rows, heads, D)
+    _kv_tensor(q, "q", q.dtype, shape, dev, True)
     if heads == 0 or heads % cache.kv_heads:
         raise ValueError(f"{heads} heads of q are no multiple of the cache's {cache.kv_heads}")
-    _kv_tensor(seq_len, "seq_len", i32, (None,), dev)
-    R = seq_len.shape[0]
-    _kv_tensor(block_table, "block_table", i32, (R, None), dev)
+    R = seq_len.numel()
+    _kv_tensor(seq_len, "seq_len", i32, (R,), dev)
+    mb = block_table.shape[-1]
+    _kv_tensor(block_table, "block_table", i32, (R, mb), dev)
     _kv_tensor(cu_new, "cu_new", i32, (R + 1,), dev)
     t = ACT_TYPES[q.dtype]
     if _elsewhere(dev, stream):
@@ -699,12 +713,11 @@ def kv_attention(cache: KvCache, q: torch.Tensor, block_table: torch.Tensor, seq
             return kv_attention(cache, q, block_table, seq_len, cu_new, scale, window, out,
                                 return_lse, ws)
     if out is None:
-        out = torch.empty((rows, heads, D), dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
     else:
-        _kv_tensor(out, "out", q.dtype, (rows, heads, D), dev, strided=True)
+        _kv_tensor(out, "out", q.dtype, shape, dev, True)
     lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
-    mb = block_table.shape[1]
-    d = KvAttnDesc(rows, R, mb, _head_rows(q), _head_rows(out), _ptr(lse), block_table.data_ptr(),
+    d = KvAttnDesc(rows, R, mb, _head_rows(q, heads), _head_rows(out, heads), _ptr(lse), block_table.data_ptr(),
                    seq_len.data_ptr(), cu_new.data_ptr(), D ** -0.5 if scale is None else scale,
                    window)
     ref = C.byref(d)

@@ -959,7 +959,7 @@ int kv_attn_check(const tq_kv_cache *c, int type, const tq_kv_attn *t, bool poin
     return fail(TQ_ESHAPE, "%s: %lld q heads, %lld output heads (need a multiple of kv_heads=%lld up to 4096, the same)",
                 what, (long long)t->q.heads, (long long)t->out.heads, (long long)c->kv_heads);
   if (t->window < 0 || t->window >= ((int64_t)1 << 31)) return fail(TQ_ESHAPE, "%s: window=%lld", what, (long long)t->window);
-  if (!(t->scale > 0.f && t->scale <= 3.4028235e38f)) return fail(TQ_EINVAL, "%s: scale must be positive and finite", what);
+  if (!(t->scale > 0.f && t->scale <= 1e30f)) return fail(TQ_EINVAL, "%s: scale must be positive, at most 1e30", what);
   if (pointers && t->rows > 0) {
     if ((rc = kv_rows_check(what, "q", &t->q, type, c->head_dim, t->rows, false)) != TQ_OK) return rc;
     if ((rc = kv_rows_check(what, "out", &t->out, type, c->head_dim, t->rows, true)) != TQ_OK) return rc;
@@ -973,7 +973,7 @@ int kv_attn_check(const tq_kv_cache *c, int type, const tq_kv_attn *t, bool poin
   a.requests = (int)t->requests;
   a.max_blocks = (int)t->max_blocks;
   a.group = (int)(t->q.heads / c->kv_heads);
-  a.window = (int)t->window;
+  a.window = (int)std::min(t->window, (int64_t)1 << 30);  // as long as a sequence can be
   a.scale = (float)((double)t->scale * 1.4426950408889634);
   a.q = kv_rows(&t->q);
   a.out = kv_rows(&t->out);

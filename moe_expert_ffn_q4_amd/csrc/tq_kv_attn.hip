@@ -37,9 +37,14 @@ constexpr int item_units(bool wide) { return wide ? 5 : 16; }
 constexpr float kLowest = -3.4028234663852886e38f;
 constexpr float kSlack = 2.f;    // see step()
 
-// A request with more query columns a kv head (new tokens x heads) than this goes to k_kv_wide, if
-// that is launched: from an average of as many a request. TODO
+// A request with more query columns a kv head (new tokens x heads) than this goes to k_kv_wide, which
+// is launched beside k_kv_attn from an average of as many a request (the lengths live on the device;
+// the launch costs about 8 us where no request is for it). Two tiles of 16 columns cost k_kv_attn
+// as much issue as k_kv_wide's workgroup costs for up to 128.
 constexpr int kWideCols = 32;
+// Query tiles of 16 columns that a wave of k_kv_wide takes (registers: two do not fit beside two
+// terms of an fp32 query or beside head_dim 256 without scratch).
+constexpr int wide_tiles(bool f32, int nb) { return nb == 8 || (f32 && nb == 4) ? 1 : 2; }
 // Workgroups of k_kv_wide per compute unit (registers: 256 a lane up to head_dim 128, 512 for 256).
 constexpr int resident_wide(int nb) { return nb <= 4 ? 2 : 1; }
 
@@ -94,13 +99,12 @@ __device__ __forceinline__ int64_t units_of(const AttnArgs &a, const Request &q)
   return (int64_t)a.g.heads * q.tiles * q.units;
 }
 
-// a / b for 0 <= a < 2^53, 0 < b < 2^31 (a 64-bit integer division takes over a hundred
-// instructions; the quotient of the doubles is off by less than one).
+// a / b for 0 <= a, 0 < b < 2^31 (a 64-bit integer division takes over a hundred instructions; the
+// quotient of the doubles is off by one at most below 2^53, by little more above).
 __device__ __forceinline__ int64_t quotient(int64_t a, int b) {
-  int64_t q = (int64_t)((double)a / (double)b);
-  const int64_t r = a - q * b;
-  if (r < 0) --q;
-  if (r >= b) ++q;
+  int64_t q = (int64_t)((double)a / (double)b), r = a - q * b;
+  for (; r < 0; r += b) --q;
+  for (; r >= b; r -= b) ++q;
   return q;
 }
 
@@ -434,6 +438,9 @@ __device__ __forceinline__ int query_exponent(float most) {
   return most > 0.f && most < INFINITY ? min(15 - __builtin_amdgcn_frexp_expf(most), 100) : 0;
 }
 
+// The softmax scale for a query times 2^e; not 0, which times a hidden token's -infinity would be no number.
+__device__ __forceinline__ float query_scale(float scale, int e) { return fmaxf(ldexpf(scale, -e), 1.17549435e-38f); }
+
 // Column `col` of a tile whose first row of q is `row`, first head head0, with `per` heads a token.
 template <typename A>
 __device__ __forceinline__ void store_out(const AttnArgs &a, int row, int head0, int per, int col, int d,
@@ -669,7 +676,7 @@ struct Attn {
       most = fmaxf(most, __shfl_xor(most, 16));
       most = fmaxf(most, __shfl_xor(most, 32));
       const int e = query_exponent(most);
-      qs = ldexpf(a.scale, -e);
+      qs = query_scale(a.scale, e);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -763,7 +770,7 @@ struct Wide {
   typedef A Act;
   typedef typename A::type T;
   static constexpr bool kWide = true;
-  static constexpr int CT = NB == 8 ? 1 : 2;
+  static constexpr int CT = wide_tiles(sizeof(T) == 4, NB);
   static constexpr int NCOL = kWaves * 16 * CT;
   static constexpr int D = 32 * NB;
   static constexpr int kPart = NCOL * (D + 2);
@@ -1123,7 +1130,7 @@ struct Wide {
       most = fmaxf(most, __shfl_xor(most, 16));
       most = fmaxf(most, __shfl_xor(most, 32));
       const int e = query_exponent(most);
-      qs[c] = ldexpf(a.scale, -e);
+      qs[c] = query_scale(a.scale, e);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         asm volatile("" ::: "memory");
@@ -1379,8 +1386,8 @@ size_t kv_attention_workspace(int type, int64_t head_dim, int64_t group, int64_t
     return (size_t)(workgroups * (2 * columns * (head_dim + 2) * 4 + (int64_t)sizeof(JoinItem)));
   };
   const size_t few = bytes(grid, split_type(type) ? 8 : 16);
-  const size_t many = wide_launch(group, rows, requests)
-                          ? bytes(kComputeUnits * resident_wide((int)(head_dim / 32)), head_dim == 256 ? 64 : 128) : 0;
+  const int nb = (int)(head_dim / 32), columns = kWaves * 16 * wide_tiles(type == TQ_F32, nb);
+  const size_t many = wide_launch(group, rows, requests) ? bytes(kComputeUnits * resident_wide(nb), columns) : 0;
   return few > many ? few : many;
 }
 

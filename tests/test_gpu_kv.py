@@ -557,6 +557,47 @@ def test_attention_query_that_is_not_a_number():
         assert np.isnan(out[bad]).all() and np.array_equal(out[~bad], clean[~bad])
 
 
+def test_attention_prompt_query_that_is_not_a_number():
+    _case("attention prompt nan query")
+    g = np.random.default_rng(19)
+    b = Batch(g, 1, 64, 16, [90])
+    for t in TYPES:
+        x = g.standard_normal((50, 4, 64))
+        bad = np.zeros((50, 4), bool)
+        bad[3, 1] = bad[47, 2] = True
+        x2 = x.copy()
+        x[3, 1, 7], x[47, 2, 60] = np.nan, np.inf
+        x2[bad] = 0
+        out, _ = run_attention(b, rounded(x, t)[0], [50])
+        clean, _ = run_attention(b, rounded(x2, t)[0], [50])
+        assert np.isnan(out[bad]).all() and np.array_equal(out[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+def test_attention_tiny_scale(t):
+    """A scale and queries so small that every logit is 0, beside hidden tokens: plain means."""
+    _case("attention tiny scale", t)
+    g = np.random.default_rng(20)
+    b = Batch(g, 1, 64, 16, [45, 60])
+    for news in ([2, 1], [45, 40]):
+        q, q64 = rounded(1e-7 * g.standard_normal((sum(news), 4, 64)), t)
+        if t != "f16":
+            q, q64 = rounded(1e-30 * g.standard_normal((sum(news), 4, 64)), t)
+        out, lse = run_attention(b, q, news, scale=1e-25)
+        check_attention(b, q64, out, lse, news, t, 1e-25, 0)
+
+
+def test_attention_a_window_past_every_token():
+    """The largest window there is, with more new tokens than the sequence has."""
+    _case("attention large window")
+    g = np.random.default_rng(21)
+    b = Batch(g, 1, 64, 16, [3, 50])
+    for t in TYPES:
+        q, q64 = rounded(g.standard_normal((52, 2, 64)), t)
+        out, lse = run_attention(b, q, [5, 47], window=2**31 - 1)
+        check_attention(b, q64, out, lse, [5, 47], t, 64**-0.5, 0)
+
+
 def test_attention_pages_outside_the_cache():
     """Their tokens count as masked; nothing outside the cache is read."""
     _case("attention bad pages")

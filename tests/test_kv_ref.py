@@ -187,7 +187,7 @@ def _attn(**kw):
     (dict(q=(4096, 0, 512, 128)), 2), (dict(out=(8192, 2, 512, 128)), 2),
     (dict(q=(4096, 4098, 512, 128), out=(4096, 4098, 512, 128)), 2), (dict(window=-1), 2),
     (dict(window=1 << 31), 2), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
-    (dict(scale=float("inf")), 1), (dict(q=(None, 4, 512, 128)), 1), (dict(out=(None, 4, 512, 128)), 1),
+    (dict(scale=float("inf")), 1), (dict(scale=2e30), 1), (dict(q=(None, 4, 512, 128)), 1), (dict(out=(None, 4, 512, 128)), 1),
     (dict(q=(4098, 4, 512, 128)), 3), (dict(table=None), 1), (dict(seq=None), 1), (dict(cu=None), 1),
     (dict(table=4097), 3), (dict(lse=4098), 3), (dict(rows=3, out=(8192, 4, 500, 128)), 2),
     (dict(rows=3, out=(8192, 4, 512, 100)), 2), (dict(q=(4096, 4, -4, 128)), 2),
@@ -257,3 +257,21 @@ def test_binding_refuses():
         tq.Rope(torch.zeros(4), sections=[1, 2])
     with pytest.raises(ValueError):
         tq.Rope(torch.zeros(4).double())
+
+
+def test_kernels_use_no_scratch():
+    """The compiled kernels of the cache keep everything in registers, at the occupancy that their
+    launches count on."""
+    import re
+
+    from moe_expert_ffn_q4_amd import build
+
+    least = [(r"k_kv_attnI\w+Li[234]E", 3), (r"k_kv_attnI\w+Li8E", 2), (r"k_kv_wideI\w+Li[234]E", 2),
+             (r"k_kv_wideI\w+Li8E", 1), (r"k_kv_(plan|append|read|join)", 4)]
+    resources = build.kernel_resources()
+    for pattern, occupancy in least:
+        hits = {k: v for k, v in resources.items() if re.search(pattern, k)}
+        assert hits, pattern
+        for name, r in hits.items():
+            assert r["scratch"] == 0, f"{name}: {r['scratch']} bytes of scratch per lane"
+            assert r["occupancy"] >= occupancy, f"{name}: occupancy {r['occupancy']} < {occupancy}"
