@@ -26,10 +26,11 @@ __device__ __forceinline__ int run_of(const int32_t *off, int n, int i) {
 
 // Prefix sums over the requests of new tokens, needed pages and released pages; then every row,
 // needed page and released page finds its request by bisection. Bound by latency (two dependent
-// reads, the scan's barriers, the bisection): each workgroup repeats the scan of at most 4096
-// requests from L2 rather than wait for another one's, so a step is a single launch. Nothing reads
-// what another workgroup of the launch writes: pages on the stack above free_count are read from
-// the ended requests' table rows, which the launch leaves alone.
+// reads, the scan's barriers, the bisection: 4.2 us for 8 requests, 9.8 us for 512 and 16384 rows):
+// each workgroup repeats the scan of at most 4096 requests from L2 rather than wait for another
+// one's, so a step is a single launch. Nothing reads what another workgroup of the launch writes:
+// pages on the stack above free_count are read from the ended requests' table rows, which the launch
+// leaves alone.
 __global__ __launch_bounds__(kThreads) void k_kv_plan(PlanArgs a) {
   extern __shared__ int32_t plan_lds[];
   __shared__ int64_t wave_sum[3][kThreads / 64];
@@ -206,6 +207,8 @@ __device__ __forceinline__ void turn_pairs(F (&lo)[W], F (&hi)[W], const C *t, b
 // of 64 + 16 heads). q heads go from global memory to global memory, k and v heads into LDS as fp32,
 // from where sixteen lanes round a block of 32 (lane c holds its values c and c + 16, the two
 // nibbles of one byte). W pairs are turned per thread step, 16 bytes of a run where the rows allow.
+// 8192 rows bf16, 64 + 16 heads of 128: 77 us, 4.0 TB/s of 311 MB; vector issue takes half of it and
+// the waves wait for memory and at the two barriers for most of the rest. One row: 6 us, of latency.
 template <typename A, int W, int NB>
 __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a, int rb, int hg) {
   typedef typename A::type T;
@@ -288,8 +291,13 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a, int rb, in
     load_run<A, W, (W > 1)>(x + e0, lo);
     load_run<A, W, (W > 1)>(x + e1, hi);
     if (turned) turn_pairs<float, float2, W>(lo, hi, turn32 + row * pairs + u * W, a.interleaved);
-    store_run<A, W, (W > 1)>(y + e0, lo);
-    store_run<A, W, (W > 1)>(y + e1, hi);
+    if constexpr (W > 1) {
+      store_run_past<A, W>(y + e0, lo);
+      store_run_past<A, W>(y + e1, hi);
+    } else {
+      y[e0] = A::from(lo[0]);
+      y[e1] = A::from(hi[0]);
+    }
   }
   __syncthreads();
   // a group of sixteen lanes takes a row's head, block by block
@@ -354,7 +362,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a, int rb, in
 // One thread: eight neighbouring values of one row and head, keys and values, so that a wave stores
 // whole lines. The quants (of a value row: a byte of each of sixteen dwords a block, which four
 // tokens share) come through LDS, fetched 16 bytes a lane: read byte by byte from global memory, the
-// loads' address work took the whole time (66 cycles an instruction; 119 us for 65536 rows).
+// loads' address work took the whole time (66 cycles an instruction; 119 us for 65536 rows). Bound by
+// HBM: 65536 rows bf16 of 8 heads of 128 take 64 us, 5.4 TB/s of 344 MB.
 template <typename A, int NB>
 __global__ __launch_bounds__(kThreads) void k_kv_read(ReadArgs a, int rows_per_wg) {
   typedef typename A::type T;
@@ -394,7 +403,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(ReadArgs a, int rows_per_w
       float v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = there ? d * (float)((int)(byte[k] >> (4 * half) & 15u) - 8) : 0.f;
-      store_run<A, 8, true>((T *)dst + out, v);
+      store_run_past<A, 8>((T *)dst + out, v);
     };
     uint32_t byte[8];
     if (a.k) {
@@ -418,15 +427,15 @@ int launch_append(const AppendArgs &a, hipStream_t s) {
   constexpr int kRun = 16 / (int)sizeof(typename A::type);  // elements of a 16-byte run
   const int pairs = a.inv_freq ? a.pairs : 0;
   auto lds = [&](int rb, int hg) { return rb * (pairs * 24 + 16 + 2 * hg * a.head_dim * 4); };
-  // few rows: one row and head per workgroup (latency); many: four rows share the sines of eight
-  // heads, within 60 KB of LDS
+  // few rows: one row and head per workgroup (latency); many: up to four rows and eight heads, which
+  // share a row's sines, within 20 KB of LDS, so that registers and not LDS bound the workgroups of a
+  // compute unit (8192 rows of 64 + 16 heads of 128: 81 us with two rows in 20 KB, 87 us with four in
+  // 39 KB; 1501 rows of head_dim 64, which stay within it: 15.7 us with four rows, 17.4 us with two)
   int rb = 1, hg = 1;
   if ((int64_t)a.rows * a.g.heads > 1024) {
-    rb = 4;
-    hg = 8;
-    while (hg > 1 && lds(rb, hg) > 60 * 1024) hg >>= 1;
+    hg = a.g.heads < 8 ? a.g.heads : 8;
+    for (rb = 4; rb > 1 && lds(rb, hg) > 20 * 1024;) rb >>= 1;
   }
-  hg = hg < a.g.heads ? hg : a.g.heads;
   const dim3 grid((a.rows + rb - 1) / rb, (a.g.heads + hg - 1) / hg);
   auto fits = [](const HeadRows &h) {
     return h.data == nullptr || ((uintptr_t)h.data % 16 == 0 && h.row_stride % kRun == 0 && h.head_stride % kRun == 0);
