@@ -725,7 +725,8 @@ def kv_attention(cache: KvCache, q: torch.Tensor, block_table: torch.Tensor, seq
         need = cache.attn_bytes.get((t, rows, R, heads, mb))
         if need is None:
             need = int(lib().tq_kv_attention_workspace_bytes(cache.ref, t, ref))
-            cache.attn_bytes[t, rows, R, heads, mb] = need
+            if need:  # 0: an argument that the call below refuses
+                cache.attn_bytes[t, rows, R, heads, mb] = need
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     rc = lib().tq_kv_attention(cache.ref, t, ref, ws.data_ptr() or None,
                                ws.numel() * ws.element_size(), _raw_stream(dev.index))

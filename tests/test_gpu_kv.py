@@ -666,6 +666,21 @@ def test_attention_on_two_streams():
             assert np.array_equal(host(o.double()), want[i][0])
 
 
+@pytest.mark.parametrize("bad", [{"scale": -1.0}, {"window": -1}])
+def test_attention_after_a_refused_call(bad):
+    """A refused call leaves nothing behind: the next one of the same sizes runs."""
+    _case(f"attention refused {bad}")
+    g = np.random.default_rng(14)
+    b = Batch(g, 2, 64, 16, [40, 3])
+    q, q64 = rounded(g.standard_normal((2, 4, 64)), "f32")
+    cache = cache_of(b.data, b.lay, b.page)
+    args = (q, i32(b.table), i32(b.lens), i32([0, 1, 2]))
+    with pytest.raises(tq.TQError):
+        tq.kv_attention(cache, *args, **bad)
+    out, lse = tq.kv_attention(cache, *args, return_lse=True)
+    check_attention(b, q64, host(out.double()), host(lse), [1, 1], "f32", 0.125, 0)
+
+
 # ---- a run of them ------------------------------------------------------------------------------------
 
 def test_decode_steps_captured():
