@@ -442,10 +442,10 @@ typedef struct {
 int tq_kv_plan(const tq_kv_cache *cache, const tq_kv_step *step, void *stream);
 
 /* Rotary positions: pair p of a head turns by positions[axis][row] * inv_freq[p] (angle, cosine and
- * sine formed in fp64), (a, b) -> (a cos - b sin, a sin + b cos), keys in fp64, queries in fp32. Pair p is the elements (2p, 2p+1) with interleaved
- * set, else (p, p + pairs); elements from 2*pairs on stay. axes 1..4 (time, height, width ...):
- * the first sections[0] pairs take their position from axis 0, the next sections[1] from axis 1,
- * and so on; the sections add up to pairs. */
+ * sine formed in fp64), (a, b) -> (a cos - b sin, a sin + b cos), keys in fp64, queries in fp32.
+ * Pair p is the elements (2p, 2p+1) with interleaved set, else (p, p + pairs); elements from 2*pairs
+ * on stay. axes 1..4 (time, height, width ...): the first sections[0] pairs take their position from
+ * axis 0, the next sections[1] from axis 1, and so on; the sections add up to pairs. */
 typedef struct {
   const float *inv_freq;    /* device [pairs] */
   const int32_t *positions; /* device [axes][rows], axis_stride elements from axis to axis */
